@@ -137,7 +137,12 @@ def prepare(case, seed):
         s["mask"] = torch.rand(t, generator=gen, device="cuda") >= 0.03  # padding tokens are False
         if t < 32:
             s["mask"].fill_(True)
-        if op == "route_bwd":
+        if op == "route":
+            k = case["top"]
+            i32 = dict(dtype=torch.int32, device="cuda")
+            s["out"] = (torch.empty(t, k, **i32), torch.empty(t, k, device="cuda"), torch.empty(e, **i32), torch.empty(e + 1, **i32),
+                        torch.empty(t, k, **i32), torch.empty(t * k, **i32), torch.empty(1, device="cuda"), torch.empty(1, **i32))
+        else:
             s["routed"] = _route_plain(s["logits"], s["mask"], case["top"], case["renorm"])
             s["dweights"] = randn(t, case["top"])
             s["dloss"] = torch.full((1,), 0.01 * t, device="cuda")  # the training loss is summed over tokens
@@ -258,7 +263,7 @@ def run(state):
                                                    workspace=s["workspace"])}
         if op == "route":
             return dict(gmi.moe_route(s["logits"], s["top"], mask=s["mask"], renormalize=s["renorm"],
-                                      workspace=s["workspace"])._asdict())
+                                      out=gmi.Routing(*s["out"]), workspace=s["workspace"])._asdict())
         gmi.moe_route_bwd(s["logits"], s["routed"]["indices"], s["routed"]["weights"], s["routed"]["offsets"],
                           s["routed"]["live"], s["dweights"], s["dloss"], mask=s["mask"], renormalize=s["renorm"],
                           dlogits=s["dlogits"])
