@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import pathlib
+from typing import NamedTuple
 
 import torch
 
@@ -20,7 +21,7 @@ LIB_PATH = _PKG / "libgmi.so"
 GMI_OK, GMI_ERR_INVALID_ARG, GMI_ERR_UNSUPPORTED, GMI_ERR_MISALIGNED, GMI_ERR_WORKSPACE, GMI_ERR_HIP = range(6)
 STATUS_NAMES = ["GMI_OK", "GMI_ERR_INVALID_ARG", "GMI_ERR_UNSUPPORTED", "GMI_ERR_MISALIGNED", "GMI_ERR_WORKSPACE",
                 "GMI_ERR_HIP"]
-GMI_F16, GMI_BF16, GMI_F8E4M3 = 0, 1, 2
+GMI_F16, GMI_BF16, GMI_F8E4M3, GMI_F32 = 0, 1, 2, 3
 _DT = {torch.float16: GMI_F16, torch.bfloat16: GMI_BF16, torch.float8_e4m3fn: GMI_F8E4M3}
 
 
@@ -95,6 +96,29 @@ def lib() -> ctypes.CDLL:
     L.gmi_conv2d_fprop_implicit.argtypes = [_i32] * 13 + [_p, _p, _p, _p, ctypes.c_int, _f32, _f32, _p]
     L.gmi_time_next_gemm.restype = ctypes.c_int
     L.gmi_time_next_gemm.argtypes = [_p, _p]
+    L.gmi_rmsnorm_quant.restype = ctypes.c_int
+    L.gmi_rmsnorm_quant.argtypes = [_i32, _i32, _p, _i64, _p, _i64, _p, _f32, ctypes.c_int, _p, _i64, _p, _i64, _p,
+                                    _i64, _p, _i64, _p]
+    L.gmi_rmsnorm_bwd_workspace_bytes.restype = _sz
+    L.gmi_rmsnorm_bwd_workspace_bytes.argtypes = [_i32, _i32]
+    L.gmi_rmsnorm_bwd.restype = ctypes.c_int
+    L.gmi_rmsnorm_bwd.argtypes = [_i32, _i32, _p, _i64, _p, _i64, _p, _p, _i64, _f32, ctypes.c_int, _p, _i64, _p, _p,
+                                  _sz, _p]
+    L.gmi_gemm_f8_block_workspace_bytes.restype = _sz
+    L.gmi_gemm_f8_block_workspace_bytes.argtypes = [_i32] * 3
+    L.gmi_gemm_f8_block.restype = ctypes.c_int
+    L.gmi_gemm_f8_block.argtypes = [_i32, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _sz, _p]
+    L.gmi_gemm_f8_block_grouped_workspace_bytes.restype = _sz
+    L.gmi_gemm_f8_block_grouped_workspace_bytes.argtypes = [_i32]
+    L.gmi_gemm_f8_block_grouped.restype = ctypes.c_int
+    L.gmi_gemm_f8_block_grouped.argtypes = [_i32, _p, _i32, _i32, _i32, _p, _i64, _p, _i64, _p, _i64, _i64, _p, _i64,
+                                            _i64, _p, _i64, _p, _sz, _p]
+    L.gmi_moe_route_workspace_bytes.restype = _sz
+    L.gmi_moe_route_workspace_bytes.argtypes = [_i32, _i32]
+    L.gmi_moe_route.restype = ctypes.c_int
+    L.gmi_moe_route.argtypes = [_i32, _i32, _i32, _p, _i64, ctypes.c_int, _p, _i32] + [_p] * 9 + [_sz, _p]
+    L.gmi_moe_route_bwd.restype = ctypes.c_int
+    L.gmi_moe_route_bwd.argtypes = [_i32, _i32, _i32, _p, _i64, ctypes.c_int, _p, _i32] + [_p] * 7 + [_i64, _p]
     _lib = L
     return L
 
@@ -373,3 +397,233 @@ def conv2d_wgrad(x: torch.Tensor, dy: torch.Tensor, R: int, S: int, pad=(0, 0), 
                                            _DT[x.dtype],
                                            alpha, beta, workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return dw
+
+
+# ---------------------------------------------------------------- block-scaled fp8 mixture-of-experts layer
+BLOCK = 128  # columns (and weight rows) per scale
+
+
+def _scale_blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor this call makes.  It belongs to the current stream; if the work runs on another one, the allocator
+    is told, so that its memory is not handed out again before that work is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        t.record_stream(s)
+    return t
+
+
+def _scratch(workspace, need: int, device, stream):
+    """(address, bytes) of the caller's workspace, or of one made for this call (None without need)."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = _new(need, torch.uint8, device, stream)
+        # the launch reads the address only, and the memory is reused in stream order
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype) -> int:
+    """Checks a device matrix with unit stride along its rows; returns its leading dimension."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {dtype} [{rows}][{cols}], got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the device")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    # with at most one row the stride says nothing: any legal leading dimension does
+    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype) -> int:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous device tensor of {n} {dtype}")
+    return t.data_ptr()
+
+
+def _mask(mask, tokens: int):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError("mask must be bool or uint8")
+    return _vector(mask, "mask", tokens, mask.dtype)
+
+
+def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                  h: torch.Tensor | None = None, y: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                  scales: torch.Tensor | None = None, quantize: bool = True, stream=None):
+    """h = x + residual; v = weight * h / sqrt(mean(h^2) + eps); q = e4m3(v / s) with one fp32 scale s per row and
+    128 columns.  x [rows][K] float16 or bfloat16.  `h` (the sum, in x's type; may be x or residual) and `y` (v in
+    x's type) are written where given.  Returns (q, scales), float8_e4m3fn [rows][K] and float32
+    [rows][ceil(K / 128)]; with quantize=False only `y` (made if not given) is written and returned."""
+    rows, K = x.shape
+    dt = x.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError("x must be float16 or bfloat16")
+    ldx = _matrix(x, "x", rows, K, dt)
+    if quantize:
+        if q is None:
+            q = _new((rows, K), torch.float8_e4m3fn, x.device, stream)
+        if scales is None:
+            scales = _new((rows, _scale_blocks(K)), torch.float32, x.device, stream)
+        ldq = _matrix(q, "q", rows, K, torch.float8_e4m3fn)
+        lds = _matrix(scales, "scales", rows, _scale_blocks(K), torch.float32)
+    else:
+        if q is not None or scales is not None:
+            raise ValueError("q and scales are written with quantize=True only")
+        if y is None:
+            y = _new((rows, K), dt, x.device, stream)
+        ldq = lds = 0
+    ldr = _matrix(residual, "residual", rows, K, dt) if residual is not None else 0
+    ldh = _matrix(h, "h", rows, K, dt) if h is not None else 0
+    ldy = _matrix(y, "y", rows, K, dt) if y is not None else 0
+    _check(lib().gmi_rmsnorm_quant(rows, K, x.data_ptr(), ldx, _ptr(residual), ldr, _vector(weight, "weight", K, dt),
+                                   eps, _DT[dt], _ptr(h), ldh, _ptr(y), ldy, _ptr(q), ldq, _ptr(scales), lds,
+                                   _stream(stream)))
+    return (q, scales) if quantize else y
+
+
+def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dres: torch.Tensor | None = None,
+                eps: float = 1e-6, dh: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of rmsnorm_quant's norm: `dy` is that of v, `h` the sum the forward wrote, `dres` the gradient that
+    reaches h past the norm.  Returns (dh, dweight): dh in h's type (the gradient of x and of residual), dweight
+    float32 [K]."""
+    rows, K = h.shape
+    dt = h.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise ValueError("h must be float16 or bfloat16")
+    if dh is None:
+        dh = _new((rows, K), dt, h.device, stream)
+    if dweight is None:
+        dweight = _new((K,), torch.float32, h.device, stream)
+    ws, nbytes = _scratch(workspace, lib().gmi_rmsnorm_bwd_workspace_bytes(rows, K) if workspace is None else 0,
+                          h.device, stream)
+    _check(lib().gmi_rmsnorm_bwd(rows, K, dy.data_ptr(), _matrix(dy, "dy", rows, K, dt), h.data_ptr(),
+                                 _matrix(h, "h", rows, K, dt), _vector(weight, "weight", K, dt), _ptr(dres),
+                                 _matrix(dres, "dres", rows, K, dt) if dres is not None else 0, eps, _DT[dt],
+                                 dh.data_ptr(), _matrix(dh, "dh", rows, K, dt),
+                                 _vector(dweight, "dweight", K, torch.float32), ws, nbytes, _stream(stream)))
+    return dh, dweight
+
+
+def _f8_out(Y, rows: int, N: int, device, stream) -> torch.Tensor:
+    if Y is not None:
+        return Y
+    return _new((rows, (N + 7) // 8 * 8), torch.bfloat16, device, stream)[:, :N]
+
+
+def gemm_f8_block(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                  Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W^T over block-scaled fp8: X float8_e4m3fn [M][K] with x_scales float32 [M][ceil(K / 128)], W
+    float8_e4m3fn [N][K] with w_scales float32 [ceil(N / 128)][ceil(K / 128)]; Y bfloat16 [M][N].  `workspace` as
+    for gemm_w4a16 (an empty tensor runs unsplit)."""
+    M, K = X.shape
+    N = W.shape[0]
+    f8, kb = torch.float8_e4m3fn, _scale_blocks(K)
+    Y = _f8_out(Y, M, N, X.device, stream)
+    ws, nbytes = _scratch(workspace, lib().gmi_gemm_f8_block_workspace_bytes(M, N, K) if workspace is None else 0,
+                          X.device, stream)
+    _check(lib().gmi_gemm_f8_block(M, N, K, X.data_ptr(), _matrix(X, "X", M, K, f8), x_scales.data_ptr(),
+                                   _matrix(x_scales, "x_scales", M, kb, torch.float32), W.data_ptr(),
+                                   _matrix(W, "W", N, K, f8), w_scales.data_ptr(),
+                                   _matrix(w_scales, "w_scales", _scale_blocks(N), kb, torch.float32), Y.data_ptr(),
+                                   _matrix(Y, "Y", M, N, torch.bfloat16), ws or None, nbytes, _stream(stream)))
+    return Y
+
+
+def gemm_f8_block_grouped(offsets: torch.Tensor, X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor,
+                          w_scales: torch.Tensor, Y: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gemm_f8_block per group: rows offsets[g] .. offsets[g + 1] of X and Y belong to group g with weight W[g] (W
+    [groups][N][K]) and scales w_scales[g].  `offsets` is a device int32 tensor of groups + 1 entries, as moe_route
+    writes it; rows outside every group are not written."""
+    rows, K = X.shape
+    if W.dim() != 3 or w_scales.dim() != 3 or w_scales.shape[0] != W.shape[0]:
+        raise ValueError("W must be [groups][N][K] and w_scales [groups][ceil(N / 128)][ceil(K / 128)]")
+    count, N, _ = W.shape
+    f8, kb = torch.float8_e4m3fn, _scale_blocks(K)
+    if count == 0:
+        return _f8_out(Y, rows, N, X.device, stream)
+    Y = _f8_out(Y, rows, N, X.device, stream)
+    ws, nbytes = _scratch(workspace, lib().gmi_gemm_f8_block_grouped_workspace_bytes(count) if workspace is None
+                          else 0, X.device, stream)
+    _check(lib().gmi_gemm_f8_block_grouped(
+        count, _vector(offsets, "offsets", count + 1, torch.int32), rows, N, K, X.data_ptr(),
+        _matrix(X, "X", rows, K, f8), x_scales.data_ptr(), _matrix(x_scales, "x_scales", rows, kb, torch.float32),
+        W.data_ptr(), _matrix(W[0], "W[0]", N, K, f8), W.stride(0), w_scales.data_ptr(),
+        _matrix(w_scales[0], "w_scales[0]", _scale_blocks(N), kb, torch.float32), w_scales.stride(0), Y.data_ptr(),
+        _matrix(Y, "Y", rows, N, torch.bfloat16), ws, nbytes, _stream(stream)))
+    return Y
+
+
+class Routing(NamedTuple):
+    """What moe_route writes, int32 unless said otherwise: the experts of each token and their float32 weights
+    [tokens][k], rows per expert, the row offsets [experts + 1] of the grouped calls, the row of each slot
+    [tokens][k], the slot of each row [tokens * k], the balance loss (float32 [1]) and the live tokens [1]."""
+    indices: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    slot_row: torch.Tensor
+    row_slot: torch.Tensor
+    loss: torch.Tensor
+    live: torch.Tensor
+
+
+_LOGITS = {torch.float16: GMI_F16, torch.bfloat16: GMI_BF16, torch.float32: GMI_F32}
+
+
+def _logits(t: torch.Tensor):
+    if t.dim() != 2 or t.dtype not in _LOGITS:
+        raise ValueError("logits must be [tokens][experts] in float16, bfloat16 or float32")
+    return _matrix(t, "logits", t.shape[0], t.shape[1], t.dtype)
+
+
+def moe_route(logits: torch.Tensor, k: int, mask: torch.Tensor | None = None, renormalize: bool = True,
+              out: Routing | None = None, workspace: torch.Tensor | None = None, stream=None) -> Routing:
+    """Top-k routing of logits [tokens][experts] with the balance loss; see Routing.  `mask` (bool or uint8
+    [tokens]) leaves tokens out: their slots hold expert -1.  `out` receives the results where given."""
+    T, E = logits.shape
+    ld = _logits(logits)
+    if out is None:
+        dev, i32, f32 = logits.device, torch.int32, torch.float32
+        out = Routing(_new((T, k), i32, dev, stream), _new((T, k), f32, dev, stream), _new((E,), i32, dev, stream),
+                      _new((E + 1,), i32, dev, stream), _new((T, k), i32, dev, stream), _new((T * k,), i32, dev, stream),
+                      _new((1,), f32, dev, stream), _new((1,), i32, dev, stream))
+    sizes = (T * k, T * k, E, E + 1, T * k, T * k, 1, 1)
+    ptrs = [_vector(t, name, n, torch.float32 if name in ("weights", "loss") else torch.int32)
+            for t, name, n in zip(out, Routing._fields, sizes)]
+    ws, nbytes = _scratch(workspace, lib().gmi_moe_route_workspace_bytes(T, E) if workspace is None else 0,
+                          logits.device, stream)
+    _check(lib().gmi_moe_route(T, E, k, logits.data_ptr(), ld, _LOGITS[logits.dtype], _mask(mask, T),
+                               int(renormalize), *ptrs, ws, nbytes, _stream(stream)))
+    return out
+
+
+def moe_route_bwd(logits: torch.Tensor, indices: torch.Tensor, weights: torch.Tensor, offsets: torch.Tensor,
+                  live: torch.Tensor, dweights: torch.Tensor, dloss: torch.Tensor, mask: torch.Tensor | None = None,
+                  renormalize: bool = True, dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route's logits from `dweights` [tokens][k] (float32) and `dloss` (float32 [1], on the
+    device), with what the forward call wrote; mask and renormalize as given to it."""
+    T, E = logits.shape
+    ld = _logits(logits)
+    k = indices.shape[-1]
+    if dlogits is None:
+        dlogits = _new((T, E), logits.dtype, logits.device, stream)
+    ldd = _matrix(dlogits, "dlogits", T, E, logits.dtype)
+    _check(lib().gmi_moe_route_bwd(T, E, k, logits.data_ptr(), ld, _LOGITS[logits.dtype], _mask(mask, T),
+                                   int(renormalize), _vector(indices, "indices", T * k, torch.int32),
+                                   _vector(weights, "weights", T * k, torch.float32),
+                                   _vector(offsets, "offsets", E + 1, torch.int32),
+                                   _vector(live, "live", 1, torch.int32),
+                                   _vector(dweights, "dweights", T * k, torch.float32),
+                                   _vector(dloss, "dloss", 1, torch.float32), dlogits.data_ptr(), ldd,
+                                   _stream(stream)))
+    return dlogits

@@ -13,7 +13,8 @@ PKG = pathlib.Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libgmi.so"
 OBJDIR = PKG / "_build"
-SOURCES = ["gmi_api.hip", "kernels_gemm.hip", "kernels_conv.hip", "kernels_w4a16.hip"]
+SOURCES = ["gmi_api.hip", "kernels_gemm.hip", "kernels_conv.hip", "kernels_w4a16.hip", "kernels_norm.hip",
+           "kernels_f8block.hip", "kernels_route.hip"]
 ARCH = "gfx950"
 
 

@@ -750,4 +750,309 @@ gmi_status gmi_conv2d_fprop_implicit_fused(int32_t N, int32_t H, int32_t W, int3
                     alpha, beta, (int)act, stream);
 }
 
+// ---------------------------------------------------------------------------
+// block-scaled fp8 mixture-of-experts layer
+// ---------------------------------------------------------------------------
+// a row operand of the norm calls: [rows][ld], 16-bit, 128-bit accesses
+static gmi_status norm_operand(const char* who, const char* name, const void* p, int64_t ld, int32_t K) {
+  if (!p) return fail(GMI_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+  if (ld < K) return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension of %s below K", who, name);
+  if (!aligned16(p) || ld % 8)
+    return fail(GMI_ERR_MISALIGNED, "%s: %s must be 16-byte aligned, its leading dimension a multiple of 8", who, name);
+  return GMI_OK;
+}
+
+static gmi_status norm_sizes(const char* who, int32_t rows, int32_t K, float eps, gmi_dtype dtype) {
+  if (rows < 0 || K < 1) return fail(GMI_ERR_INVALID_ARG, "%s: rows %d < 0 or K %d < 1", who, rows, K);
+  if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(GMI_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
+  if (!dtype_ok(dtype)) return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
+  if (K > kMaxNormK) return fail(GMI_ERR_UNSUPPORTED, "%s: K %d above %d", who, K, kMaxNormK);
+  if (K % 8) return fail(GMI_ERR_MISALIGNED, "%s: K must be a multiple of 8 (128-bit accesses)", who);
+  return GMI_OK;
+}
+
+gmi_status gmi_rmsnorm_quant(int32_t rows, int32_t K, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                             const void* weight, float eps, gmi_dtype dtype, void* h, int64_t ldh, void* y,
+                             int64_t ldy, void* q, int64_t ldq, float* scales, int64_t lds, void* stream) {
+  g_last_error.clear();
+  const char* who = "rmsnorm_quant";
+  gmi_status st = norm_sizes(who, rows, K, eps, dtype);
+  if (st != GMI_OK) return st;
+  if (rows == 0) return GMI_OK;
+  if (!y && !q) return fail(GMI_ERR_INVALID_ARG, "%s: neither y nor q is wanted", who);
+  if ((q == nullptr) != (scales == nullptr))
+    return fail(GMI_ERR_INVALID_ARG, "%s: q and scales go together", who);
+  if ((st = norm_operand(who, "x", x, ldx, K)) != GMI_OK ||
+      (st = norm_operand(who, "weight", weight, K, K)) != GMI_OK ||
+      (residual && (st = norm_operand(who, "residual", residual, ldr, K)) != GMI_OK) ||
+      (h && (st = norm_operand(who, "h", h, ldh, K)) != GMI_OK) ||
+      (y && (st = norm_operand(who, "y", y, ldy, K)) != GMI_OK))
+    return st;
+  if (q) {
+    if (ldq < K || lds < cdiv(K, 128))
+      return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension of q below K or of scales below ceil(K / 128)", who);
+    if (((uintptr_t)q & 7u) || ldq % 8 || ((uintptr_t)scales & 3u))
+      return fail(GMI_ERR_MISALIGNED, "%s: q must be 8-byte aligned, ldq a multiple of 8, scales 4-byte aligned", who);
+  }
+  NormLaunch a;
+  a.rows = rows;
+  a.K = K;
+  a.x = (const uint16_t*)x;
+  a.residual = (const uint16_t*)residual;
+  a.weight = (const uint16_t*)weight;
+  a.h = (uint16_t*)h;
+  a.y = (uint16_t*)y;
+  a.q = (uint8_t*)q;
+  a.scales = scales;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldh = ldh;
+  a.ldy = ldy;
+  a.ldq = ldq;
+  a.lds = lds;
+  a.eps = eps;
+  return hip_status(launch_rmsnorm_quant(a, (int)dtype, (hipStream_t)stream), who);
+}
+
+size_t gmi_rmsnorm_bwd_workspace_bytes(int32_t rows, int32_t K) {
+  if (rows <= 0 || K <= 0 || K > kMaxNormK || K % 8) return 0;
+  return (size_t)norm_bwd_parts(rows, K) * (size_t)K * sizeof(float);
+}
+
+gmi_status gmi_rmsnorm_bwd(int32_t rows, int32_t K, const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                           const void* weight, const void* dres, int64_t lddr, float eps, gmi_dtype dtype, void* dh,
+                           int64_t lddh, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const char* who = "rmsnorm_bwd";
+  gmi_status st = norm_sizes(who, rows, K, eps, dtype);
+  if (st != GMI_OK) return st;
+  if ((uintptr_t)dweight & 3u) return fail(GMI_ERR_MISALIGNED, "%s: dweight must be 4-byte aligned", who);
+  if (rows > 0) {
+    if ((st = norm_operand(who, "dy", dy, lddy, K)) != GMI_OK || (st = norm_operand(who, "h", h, ldh, K)) != GMI_OK ||
+        (st = norm_operand(who, "weight", weight, K, K)) != GMI_OK ||
+        (dres && (st = norm_operand(who, "dres", dres, lddr, K)) != GMI_OK) ||
+        (st = norm_operand(who, "dh", dh, lddh, K)) != GMI_OK)
+      return st;
+    const size_t need = dweight ? gmi_rmsnorm_bwd_workspace_bytes(rows, K) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+      return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+    if (need && !aligned16(workspace)) return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
+  } else if (!dweight) {
+    return GMI_OK;
+  }
+  NormBwdLaunch a;
+  a.rows = rows;
+  a.K = K;
+  a.dy = (const uint16_t*)dy;
+  a.h = (const uint16_t*)h;
+  a.weight = (const uint16_t*)weight;
+  a.dres = (const uint16_t*)dres;
+  a.dh = (uint16_t*)dh;
+  a.partial = dweight ? (float*)workspace : nullptr;
+  a.lddy = lddy;
+  a.ldh = ldh;
+  a.lddr = lddr;
+  a.lddh = lddh;
+  a.eps = eps;
+  return hip_status(launch_rmsnorm_bwd(a, (int)dtype, dweight, (hipStream_t)stream), who);
+}
+
+// Checks shared by the block-scaled GEMM calls and the launch record they
+// fill; `nothing` is set when there is no work.
+static gmi_status f8_block_prepare(const char* who, int32_t M, int32_t N, int32_t K, const void* X, int64_t ldx,
+                                   const float* xs, int64_t ldxs, const void* W, int64_t ldw, const float* ws,
+                                   int64_t ldws, void* Y, int64_t ldy, F8BlockLaunch& a, bool& nothing) {
+  nothing = false;
+  if (M < 0 || N < 0 || K < 0) return fail(GMI_ERR_INVALID_ARG, "%s: negative size (%d, %d, %d)", who, M, N, K);
+  if (M == 0 || N == 0) {
+    nothing = true;
+    return GMI_OK;
+  }
+  if (!Y || (K > 0 && (!X || !xs || !W || !ws))) return fail(GMI_ERR_INVALID_ARG, "%s: a NULL operand", who);
+  const int64_t kb = cdiv(K, 128);
+  if (ldy < N || (K > 0 && (ldx < K || ldw < K || ldxs < kb || ldws < kb)))
+    return fail(GMI_ERR_INVALID_ARG, "%s: a leading dimension below its row width", who);
+  if (ldy > kMaxLd || (K > 0 && (ldx > kMaxLd || ldw > kMaxLd || ldxs > kMaxLd || ldws > kMaxLd)))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: a leading dimension above 2^22 elements", who);
+  if (K % 16 || (K > 0 && (ldx % 16 || ldw % 16)))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: fp8 needs K, ldx and ldw multiples of 16", who);
+  if (!aligned16(Y) || ldy % 8 ||
+      (K > 0 && (!aligned16(X) || !aligned16(W) || ((uintptr_t)xs & 3u) || ((uintptr_t)ws & 3u))))
+    return fail(GMI_ERR_MISALIGNED,
+                "%s: X, W and Y must be 16-byte aligned, scales 4-byte aligned, ldy a multiple of 8", who);
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.X = (const uint8_t*)X;
+  a.W = (const uint8_t*)W;
+  a.xs = xs;
+  a.ws = ws;
+  a.Y = (uint16_t*)Y;
+  a.ldx = ldx;
+  a.ldxs = ldxs;
+  a.ldw = ldw;
+  a.ldws = ldws;
+  a.ldy = ldy;
+  a.offsets = nullptr;
+  a.count = 0;
+  a.w_stride = a.ws_stride = 0;
+  return GMI_OK;
+}
+
+size_t gmi_gemm_f8_block_workspace_bytes(int32_t M, int32_t N, int32_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return f8_block_workspace(M, N, K);
+}
+
+gmi_status gmi_gemm_f8_block(int32_t M, int32_t N, int32_t K, const void* X, int64_t ldx, const float* x_scales,
+                             int64_t ldxs, const void* W, int64_t ldw, const float* w_scales, int64_t ldws, void* Y,
+                             int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const char* who = "gemm_f8_block";
+  F8BlockLaunch a;
+  bool nothing;
+  const gmi_status st =
+      f8_block_prepare(who, M, N, K, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, a, nothing);
+  if (st != GMI_OK || nothing) return st;
+  if (workspace && !aligned16(workspace))
+    return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
+  return hip_status(launch_f8_block(a, workspace, workspace_bytes, (hipStream_t)stream), who);
+}
+
+size_t gmi_gemm_f8_block_grouped_workspace_bytes(int32_t count) {
+  return count > 0 && count <= kMaxOffsetGroupCount ? f8_block_grouped_workspace(count) : 0;
+}
+
+gmi_status gmi_gemm_f8_block_grouped(int32_t count, const int32_t* offsets, int32_t rows, int32_t N, int32_t K,
+                                     const void* X, int64_t ldx, const float* x_scales, int64_t ldxs, const void* W,
+                                     int64_t ldw, int64_t w_stride, const float* w_scales, int64_t ldws,
+                                     int64_t ws_stride, void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  g_last_error.clear();
+  const char* who = "gemm_f8_block_grouped";
+  if (count < 0) return fail(GMI_ERR_INVALID_ARG, "%s: count %d < 0", who, count);
+  if (count > kMaxOffsetGroupCount)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: %d groups, at most %d", who, count, kMaxOffsetGroupCount);
+  F8BlockLaunch a;
+  bool nothing;
+  const gmi_status st =
+      f8_block_prepare(who, rows, N, K, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, a, nothing);
+  if (st != GMI_OK) return st;
+  if (nothing || count == 0) return GMI_OK;
+  if (!offsets) return fail(GMI_ERR_INVALID_ARG, "%s: offsets is NULL", who);
+  if ((uintptr_t)offsets & 3u) return fail(GMI_ERR_MISALIGNED, "%s: offsets must be 4-byte aligned", who);
+  if (w_stride < 0 || ws_stride < 0) return fail(GMI_ERR_INVALID_ARG, "%s: negative group stride", who);
+  if (K > 0 && count > 1 &&
+      (w_stride < (int64_t)(N - 1) * ldw + K || ws_stride < (cdiv(N, 128) - 1) * ldws + cdiv(K, 128)))
+    return fail(GMI_ERR_INVALID_ARG, "%s: a group stride is smaller than one group's data", who);
+  if (w_stride % 16) return fail(GMI_ERR_MISALIGNED, "%s: w_stride must be a multiple of 16", who);
+  const size_t need = f8_block_grouped_workspace(count);
+  if (!workspace || workspace_bytes < need)
+    return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
+  a.offsets = offsets;
+  a.count = count;
+  a.w_stride = w_stride;
+  a.ws_stride = ws_stride;
+  return hip_status(launch_f8_block_grouped(a, workspace, (hipStream_t)stream), who);
+}
+
+// checks of sizes shared by the routing calls
+static gmi_status route_sizes(const char* who, int32_t tokens, int32_t experts, int32_t k, const void* logits,
+                              int64_t ld, gmi_dtype dtype) {
+  if (tokens < 0 || experts < 1 || k < 1 || k > experts)
+    return fail(GMI_ERR_INVALID_ARG, "%s: tokens %d, experts %d, k %d (needs tokens >= 0, 1 <= k <= experts)", who,
+                tokens, experts, k);
+  if (experts > kMaxExperts || k > kMaxTopK)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: %d experts (at most %d), k %d (at most %d)", who, experts, kMaxExperts, k,
+                kMaxTopK);
+  if ((int64_t)tokens * k > INT32_MAX)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: tokens * k above 2^31 - 1", who);
+  if (!dtype_ok(dtype) && dtype != GMI_F32)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
+  if (tokens > 0) {
+    if (!logits) return fail(GMI_ERR_INVALID_ARG, "%s: logits is NULL", who);
+    if (ld < experts) return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension below experts", who);
+    if ((uintptr_t)logits & (dtype == GMI_F32 ? 3u : 1u))
+      return fail(GMI_ERR_MISALIGNED, "%s: logits must be aligned to their type", who);
+  }
+  return GMI_OK;
+}
+
+size_t gmi_moe_route_workspace_bytes(int32_t tokens, int32_t experts) {
+  if (tokens <= 0 || experts < 1 || experts > kMaxExperts) return 0;
+  return plan_route(tokens, experts).bytes;
+}
+
+gmi_status gmi_moe_route(int32_t tokens, int32_t experts, int32_t k, const void* logits, int64_t ld, gmi_dtype dtype,
+                         const uint8_t* mask, int32_t renormalize, int32_t* indices, float* weights, int32_t* counts,
+                         int32_t* offsets, int32_t* slot_row, int32_t* row_slot, float* loss, int32_t* live,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const char* who = "moe_route";
+  const gmi_status st = route_sizes(who, tokens, experts, k, logits, ld, dtype);
+  if (st != GMI_OK) return st;
+  if (!counts || !offsets || !loss || !live || (tokens > 0 && (!indices || !weights || !slot_row || !row_slot)))
+    return fail(GMI_ERR_INVALID_ARG, "%s: a NULL output", who);
+  if (((uintptr_t)indices | (uintptr_t)weights | (uintptr_t)counts | (uintptr_t)offsets | (uintptr_t)slot_row |
+       (uintptr_t)row_slot | (uintptr_t)loss | (uintptr_t)live) & 3u)
+    return fail(GMI_ERR_MISALIGNED, "%s: outputs must be 4-byte aligned", who);
+  const size_t need = gmi_moe_route_workspace_bytes(tokens, experts);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+  if (need && ((uintptr_t)workspace & 3u))
+    return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 4-byte aligned", who);
+  RouteLaunch a{};
+  a.logits = logits;
+  a.mask = mask;
+  a.ld = ld;
+  a.T = tokens;
+  a.E = experts;
+  a.k = k;
+  a.renorm = renormalize != 0;
+  a.indices = indices;
+  a.weights = weights;
+  a.counts = counts;
+  a.offsets = offsets;
+  a.slot_row = slot_row;
+  a.row_slot = row_slot;
+  a.loss = loss;
+  a.live = live;
+  return hip_status(launch_route(a, (int)dtype, workspace, (hipStream_t)stream), who);
+}
+
+gmi_status gmi_moe_route_bwd(int32_t tokens, int32_t experts, int32_t k, const void* logits, int64_t ld,
+                             gmi_dtype dtype, const uint8_t* mask, int32_t renormalize, const int32_t* indices,
+                             const float* weights, const int32_t* offsets, const int32_t* live,
+                             const float* dweights, const float* dloss, void* dlogits, int64_t ldd, void* stream) {
+  g_last_error.clear();
+  const char* who = "moe_route_bwd";
+  const gmi_status st = route_sizes(who, tokens, experts, k, logits, ld, dtype);
+  if (st != GMI_OK || tokens == 0) return st;
+  if (!indices || !weights || !offsets || !live || !dweights || !dloss || !dlogits)
+    return fail(GMI_ERR_INVALID_ARG, "%s: a NULL operand", who);
+  if (ldd < experts) return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension below experts", who);
+  if (((uintptr_t)dlogits & (dtype == GMI_F32 ? 3u : 1u)) ||
+      (((uintptr_t)indices | (uintptr_t)weights | (uintptr_t)offsets | (uintptr_t)live | (uintptr_t)dweights |
+        (uintptr_t)dloss) & 3u))
+    return fail(GMI_ERR_MISALIGNED, "%s: operands must be aligned to their types", who);
+  RouteBwdLaunch a;
+  a.logits = logits;
+  a.mask = mask;
+  a.indices = indices;
+  a.offsets = offsets;
+  a.live = live;
+  a.weights = weights;
+  a.dweights = dweights;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.ld = ld;
+  a.ldd = ldd;
+  a.T = tokens;
+  a.E = experts;
+  a.k = k;
+  a.renorm = renormalize != 0;
+  return hip_status(launch_route_bwd(a, (int)dtype, (hipStream_t)stream), who);
+}
+
 }  // extern "C"

@@ -175,4 +175,77 @@ hipError_t launch_prepack_w4(const uint8_t* w, int N, int K, uint8_t* out, hipSt
 hipError_t launch_w4a16(const W4Launch& a, hipStream_t stream);
 hipError_t launch_w4a16_grouped(const W4Grouped& a, hipStream_t stream);
 
+// RMS norm with the residual's addition; y, h, residual and q (with scales)
+// are optional
+struct NormLaunch {
+  int64_t rows;
+  int K;
+  const uint16_t *x, *residual, *weight;
+  uint16_t *h, *y;
+  uint8_t* q;
+  float* scales;
+  int64_t ldx, ldr, ldh, ldy, ldq, lds;
+  float eps;
+};
+struct NormBwdLaunch {
+  int64_t rows;
+  int K;
+  const uint16_t *dy, *h, *weight, *dres;
+  uint16_t* dh;
+  float* partial;  // one row of K weight gradients per workgroup; NULL: not wanted
+  int64_t lddy, ldh, lddr, lddh;
+  float eps;
+};
+constexpr int kMaxNormK = 32768;
+int norm_bwd_parts(int64_t rows, int K);  // rows of `partial` on the current device
+hipError_t launch_rmsnorm_quant(const NormLaunch& a, int dtype, hipStream_t stream);
+hipError_t launch_rmsnorm_bwd(const NormBwdLaunch& a, int dtype, float* dweight, hipStream_t stream);
+
+// Block-scaled fp8 GEMM Y = X W^T: dense (offsets NULL, M rows) or per group
+struct F8BlockLaunch {
+  int M, N, K;  // M: rows, or the row capacity of the grouped call
+  const uint8_t *X, *W;
+  const float *xs, *ws;
+  uint16_t* Y;
+  int64_t ldx, ldxs, ldw, ldws, ldy;
+  const int32_t* offsets;  // grouped: count + 1 row offsets on the device
+  int count;
+  int64_t w_stride, ws_stride;
+};
+size_t f8_block_workspace(int M, int N, int K);   // of the split over K; 0 without one
+size_t f8_block_grouped_workspace(int count);     // the group table
+hipError_t launch_f8_block(const F8BlockLaunch& a, void* workspace, size_t workspace_bytes, hipStream_t stream);
+hipError_t launch_f8_block_grouped(const F8BlockLaunch& a, void* workspace, hipStream_t stream);
+
+// Expert routing
+struct RouteLaunch {
+  const void* logits;
+  const uint8_t* mask;  // NULL: every token
+  int64_t ld;
+  int T, E, k, renorm;
+  int32_t *indices, *counts, *offsets, *slot_row, *row_slot, *live;
+  float *weights, *loss;
+  // several workgroups: their counts and sums of p per expert, and live tokens
+  int tokens_per_wg;
+  int32_t *wg_counts, *wg_live;
+  float* wg_psum;
+};
+struct RouteBwdLaunch {
+  const void* logits;
+  const uint8_t* mask;
+  const int32_t *indices, *offsets, *live;
+  const float *weights, *dweights, *dloss;
+  void* dlogits;
+  int64_t ld, ldd;
+  int T, E, k, renorm;
+};
+struct RoutePlan {
+  int wgs, tokens_per_wg;
+  size_t bytes;  // workspace (0 with one workgroup)
+};
+constexpr int kMaxExperts = 1024, kMaxTopK = 16;
+RoutePlan plan_route(int T, int E);
+hipError_t launch_route(const RouteLaunch& a, int dtype, void* workspace, hipStream_t stream);
+hipError_t launch_route_bwd(const RouteBwdLaunch& a, int dtype, hipStream_t stream);
+
 }  // namespace gmi

@@ -1,0 +1,522 @@
+// kernels_route.hip -- expert routing: the top-k experts of every token, their
+// weights, rows per expert with the row order the grouped GEMM calls take, and
+// the balance loss; and the gradient of the logits.
+//
+//   p = softmax(logits) over the E experts of a live token
+//   weights: p of the k largest logits (equal ones: lowest expert first), divided by their sum on request
+//   loss = E sum_e f_e P_e, f_e = counts_e / sum counts, P_e = mean of p_e over the live tokens
+// A token is live if the mask keeps it and some logit lies above -infinity;
+// an expert whose logit is -infinity (or NaN) is never taken.  Missing slots
+// hold expert -1 and weight 0 and are not counted.
+//
+// A group of L lanes (16, or 64 past 256 experts) holds one token's logits in
+// registers, V per lane, expert e = j L + lane.  Each of the k picks is a
+// maximum over V registers and four (six) lane exchanges; for 16-bit logits
+// value and expert share one 32-bit key, so that the exchange settles ties.
+// Order within an expert: a bitmask per expert over the 64 tokens of a pass
+// gives each slot its rank by counting the bits below it -- no sort, and the
+// same result on every run.
+#include "gmi_device.hpp"
+#include "gmi_internal.hpp"
+
+namespace gmi {
+
+constexpr int RT_F32 = 3;       // GMI_F32
+constexpr int RT_PASS = 64;     // tokens per pass of a workgroup
+constexpr int RT_THREADS = 1024;
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const void* p, int64_t i) {
+  if constexpr (DT == RT_F32)
+    return ((const float*)p)[i];
+  else
+    return from_bits<DT>(((const uint16_t*)p)[i]);
+}
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+// reduction over a group of L = 16 or 64 lanes, result in every lane
+template <int L, class T, class F>
+__device__ __forceinline__ T group_reduce(T v, F f) {
+  v = f(v, __builtin_bit_cast(T, dpp_i<0xB1>(__builtin_bit_cast(int, v))));
+  v = f(v, __builtin_bit_cast(T, dpp_i<0x4E>(__builtin_bit_cast(int, v))));
+  v = f(v, __builtin_bit_cast(T, dpp_i<0x141>(__builtin_bit_cast(int, v))));
+  v = f(v, __builtin_bit_cast(T, dpp_i<0x140>(__builtin_bit_cast(int, v))));
+  if constexpr (L == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<L>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+
+// Order-preserving key of a logit: larger value, larger key; 0 for values that
+// are never taken (-infinity, NaN).  -0 and +0 get the same key.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  if (!(f > -__builtin_inff())) return 0u;
+  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+// 16-bit logits: value in the upper half, the expert's complement below it
+// (the lowest expert wins a tie); E <= 1024
+template <int DT>
+__device__ __forceinline__ uint32_t packed_key(float f, int e) {
+  if (!(f > -__builtin_inff())) return 0u;
+  uint32_t u;
+  if constexpr (DT == DT_F16)
+    u = __builtin_bit_cast(uint16_t, (_Float16)(f + 0.0f));
+  else
+    u = __builtin_bit_cast(uint32_t, f + 0.0f) >> 16;
+  u = u & 0x8000u ? (~u & 0xffffu) : u | 0x8000u;
+  return u << 16 | (0xffffu - (uint32_t)e);
+}
+
+// Exclusive prefix sum over n <= 1024 values, one per thread of a
+// RT_THREADS workgroup; returns this thread's, and the total in `total`.
+__device__ __forceinline__ int block_scan(int v, int* wave_sums, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d);
+    if (lane >= d) s += o;
+  }
+  __syncthreads();
+  if (lane == 63) wave_sums[wave] = s;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < RT_THREADS / 64; ++i) {
+    const int w = wave_sums[i];
+    before += i < wave ? w : 0;
+    total += w;
+  }
+  return before + s - v;
+}
+
+// loss from the per-expert sums of p and counts (one expert per thread)
+__device__ __forceinline__ void write_loss(const RouteLaunch& a, float psum, int count, int total, int live,
+                                           float* wave_part) {
+  float v = (float)count * psum;
+  v = group_sum<64>(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) wave_part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int i = 0; i < RT_THREADS / 64; ++i) s += wave_part[i];
+    *a.loss = total > 0 ? (float)a.E * s / ((float)total * (float)live) : 0.0f;
+    *a.live = live;
+  }
+}
+
+// Routing of a contiguous range of tokens per workgroup.  Writes indices,
+// weights and each slot's rank among the workgroup's slots of its expert
+// (into slot_row), and the workgroup's counts and sums of p per expert.  With
+// a single workgroup the rest follows at once.
+template <int DT, int L, int V>
+__global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
+  constexpr int GROUPS = RT_THREADS / L, EP = L * V;
+  __shared__ uint32_t mask[RT_PASS / 32][EP];
+  __shared__ int base[EP];
+  __shared__ float psum_lds[RT_THREADS / 64][EP];
+  __shared__ int wave_i[RT_THREADS / 64];
+  __shared__ float wave_f[RT_THREADS / 64];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  for (int e = threadIdx.x; e < EP; e += RT_THREADS) {
+    base[e] = 0;
+    for (int w = 0; w < RT_PASS / 32; ++w) mask[w][e] = 0u;
+  }
+  float psum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) psum[j] = 0.0f;
+  int live_here = 0;
+  const int first = blockIdx.x * a.tokens_per_wg, end = min(a.T, first + a.tokens_per_wg);
+  __syncthreads();
+  for (int t0 = first; t0 < end; t0 += RT_PASS) {
+#pragma unroll
+    for (int sub = 0; sub < RT_PASS; sub += GROUPS) {
+      const int tl = sub + group, t = t0 + tl;
+      const bool in = t < end && (!a.mask || a.mask[t]);
+      float x[V];
+      uint32_t key[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = j * L + lane;
+        x[j] = in && e < a.E ? logit_at<DT>(a.logits, (int64_t)t * a.ld + e) : -__builtin_inff();
+        key[j] = DT == RT_F32 ? order_key(x[j]) : packed_key<DT>(x[j], e);
+      }
+      int sel = -1;
+      float top = 0.0f, val = 0.0f;
+      for (int i = 0; i < a.k; ++i) {
+        uint32_t m = key[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = m > key[j] ? m : key[j];
+        m = group_max<L>(m);
+        int e;
+        float f;
+        if constexpr (DT == RT_F32) {
+          uint32_t at = 0xffffffffu;
+#pragma unroll
+          for (int j = V - 1; j >= 0; --j) at = key[j] == m ? (uint32_t)(j * L + lane) : at;
+          e = (int)group_min<L>(at);
+#pragma unroll
+          for (int j = 0; j < V; ++j) key[j] = j * L + lane == e ? 0u : key[j];
+          f = __builtin_bit_cast(float, m & 0x80000000u ? m & 0x7fffffffu : ~m);
+        } else {
+          e = (int)(0xffffu - (m & 0xffffu));
+#pragma unroll
+          for (int j = 0; j < V; ++j) key[j] = key[j] == m ? 0u : key[j];
+          const uint32_t u = m >> 16;
+          f = from_bits<DT>(u & 0x8000u ? u & 0x7fffu : ~u & 0xffffu);
+        }
+        if (i == 0) {
+          top = f;
+          if (m == 0u) break;  // nothing to take: the token is not live
+        }
+        if (lane == i && m != 0u) {
+          sel = e;
+          val = f;
+        }
+      }
+      // not-a-number only where a live token holds one (or +infinity)
+      const bool live = group_max<L>((uint32_t)(sel >= 0)) != 0u;
+      float sum = 0.0f;
+      float p[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = j * L + lane;
+        p[j] = live && e < a.E ? __expf(x[j] - top) : 0.0f;
+        sum += p[j];
+      }
+      sum = group_sum<L>(sum);
+      const float inv = live ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) psum[j] += p[j] * inv;
+      live_here += live && lane == 0;
+      float w = sel >= 0 ? __expf(val - top) : 0.0f;
+      const float wsum = a.renorm ? group_sum<L>(w) + (sum - sum) : sum;  // a NaN of the row reaches the weights
+      w = sel >= 0 ? w / wsum : 0.0f;
+      if (t < end && lane < a.k) {
+        a.indices[(int64_t)t * a.k + lane] = sel;
+        a.weights[(int64_t)t * a.k + lane] = w;
+      }
+      if (sel >= 0) atomicOr(&mask[tl >> 5][sel], 1u << (tl & 31));
+      if constexpr (GROUPS == RT_PASS) {
+        __syncthreads();
+        if (t < end && lane < a.k) {
+          int r = -1;
+          if (sel >= 0) {
+            r = base[sel] + __popc(mask[tl >> 5][sel] & ((1u << (tl & 31)) - 1u));
+            for (int q = 0; q < tl >> 5; ++q) r += __popc(mask[q][sel]);
+          }
+          a.slot_row[(int64_t)t * a.k + lane] = r;
+        }
+      }
+    }
+    if constexpr (GROUPS != RT_PASS) {
+      // several passes filled the masks: the ranks in a second walk
+      __syncthreads();
+      const int n = min(RT_PASS, end - t0) * a.k;
+      for (int s = threadIdx.x; s < n; s += RT_THREADS) {
+        const int tl = s / a.k;
+        const int64_t slot = (int64_t)t0 * a.k + s;
+        const int sel = a.indices[slot];
+        int r = -1;
+        if (sel >= 0) {
+          r = base[sel] + __popc(mask[tl >> 5][sel] & ((1u << (tl & 31)) - 1u));
+          for (int q = 0; q < tl >> 5; ++q) r += __popc(mask[q][sel]);
+        }
+        a.slot_row[slot] = r;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < EP; e += RT_THREADS) {
+      int c = base[e];
+      for (int w = 0; w < RT_PASS / 32; ++w) {
+        c += __popc(mask[w][e]);
+        mask[w][e] = 0u;
+      }
+      base[e] = c;
+    }
+    __syncthreads();
+  }
+  // sums of p over the workgroup: the wave's groups, then the waves in order
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    float v = psum[j];
+    if constexpr (L == 16) {
+      v += __shfl_xor(v, 16);
+      v += __shfl_xor(v, 32);
+    }
+    if ((threadIdx.x & 63) < L) psum_lds[threadIdx.x >> 6][j * L + lane] = v;
+  }
+  const float lf = group_sum<64>((float)live_here);
+  if ((threadIdx.x & 63) == 0) wave_i[threadIdx.x >> 6] = (int)lf;
+  __syncthreads();
+  int live_wg = 0;
+  for (int i = 0; i < RT_THREADS / 64; ++i) live_wg += wave_i[i];
+  const int e = threadIdx.x;
+  float ps = 0.0f;
+  if (e < a.E)
+    for (int i = 0; i < RT_THREADS / 64; ++i) ps += psum_lds[i][e];
+  if (gridDim.x > 1) {
+    if (e < a.E) {
+      a.wg_counts[(int64_t)blockIdx.x * a.E + e] = base[e];
+      a.wg_psum[(int64_t)blockIdx.x * a.E + e] = ps;
+    }
+    if (e == 0) a.wg_live[blockIdx.x] = live_wg;
+    return;
+  }
+  const int cnt = e < a.E ? base[e] : 0;
+  int total;
+  const int off = block_scan(cnt, wave_i, total);
+  if (e < a.E) {
+    a.counts[e] = cnt;
+    a.offsets[e] = off;
+    base[e] = off;
+  }
+  if (e == 0) a.offsets[a.E] = total;
+  write_loss(a, ps, cnt, total, live_wg, wave_f);
+  __syncthreads();  // base now holds the offsets; ranks were written by this workgroup
+  const int slots = a.T * a.k;
+  for (int s = threadIdx.x; s < slots; s += RT_THREADS) {
+    const int x = a.indices[s];
+    if (x >= 0) {
+      const int r = base[x] + a.slot_row[s];
+      a.slot_row[s] = r;
+      a.row_slot[r] = s;
+    }
+    if (s >= total) a.row_slot[s] = -1;
+  }
+}
+
+// Second launch: every workgroup sums the count matrix for itself (totals, and
+// what lies before its own tokens), turns the ranks of its slots into rows and
+// writes both orders.  One further workgroup writes counts, offsets and loss.
+__global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int wgs) {
+  __shared__ int tot[RT_THREADS], pre[RT_THREADS], row0[RT_THREADS];
+  __shared__ float ps[RT_THREADS];
+  __shared__ int wave_i[RT_THREADS / 64];
+  __shared__ float wave_f[RT_THREADS / 64];
+  const int b = blockIdx.x;
+  const bool last = b == wgs;
+  int ep = 1;
+  while (ep < a.E) ep *= 2;
+  const int slices = RT_THREADS / ep, e = threadIdx.x % ep, sl = threadIdx.x / ep;
+  const int per = (wgs + slices - 1) / slices;
+  int st = 0, sp = 0;
+  float sf = 0.0f;
+  if (e < a.E) {
+    const int q1 = min(wgs, (sl + 1) * per);
+#pragma unroll 8
+    for (int q = sl * per; q < q1; ++q) {
+      const int c = a.wg_counts[(int64_t)q * a.E + e];
+      st += c;
+      sp += q < b ? c : 0;
+      if (last) sf += a.wg_psum[(int64_t)q * a.E + e];
+    }
+  }
+  tot[threadIdx.x] = st;
+  pre[threadIdx.x] = sp;
+  ps[threadIdx.x] = sf;
+  __syncthreads();
+  st = sp = 0;
+  sf = 0.0f;
+  if ((int)threadIdx.x < a.E) {
+    for (int s = 0; s < slices; ++s) {
+      st += tot[s * ep + threadIdx.x];
+      sp += pre[s * ep + threadIdx.x];
+      sf += ps[s * ep + threadIdx.x];
+    }
+  }
+  int total;
+  const int off = block_scan(st, wave_i, total);
+  row0[threadIdx.x] = off + sp;
+  __syncthreads();
+  if (last) {
+    if ((int)threadIdx.x < a.E) {
+      a.counts[threadIdx.x] = st;
+      a.offsets[threadIdx.x] = off;
+    }
+    if (threadIdx.x == 0) a.offsets[a.E] = total;
+    int live = 0;
+    for (int q = threadIdx.x; q < wgs; q += RT_THREADS) live += a.wg_live[q];
+    int live_all;
+    __syncthreads();
+    block_scan(live, wave_i, live_all);
+    write_loss(a, sf, st, total, live_all, wave_f);
+    return;
+  }
+  const int64_t s0 = (int64_t)b * a.tokens_per_wg * a.k;
+  const int64_t s1 = min((int64_t)a.T * a.k, s0 + (int64_t)a.tokens_per_wg * a.k);
+  for (int64_t s = s0 + threadIdx.x; s < s1; s += RT_THREADS) {
+    const int x = a.indices[s];
+    if (x >= 0) {
+      const int r = row0[x] + a.slot_row[s];
+      a.slot_row[s] = r;
+      a.row_slot[r] = (int)s;
+    }
+    if (s >= total) a.row_slot[s] = -1;  // rows past the last one; s runs over every row number too
+  }
+}
+
+// LDS written by one lane of a wave and read by another: the LDS serves a
+// wave's accesses in order, so only the compiler has to keep it
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Gradient of the logits.  dp_e = dloss E f_e / live is the loss's, the
+// weights' comes in at the taken experts: before the softmax's own derivative
+// without renormalisation, after it as that of a softmax over the taken ones
+// with it.  The k scattered values of a token go through a row of LDS that its
+// lanes share (a wave keeps its rows to itself, so no barrier).
+template <int DT, int L, int V>
+__global__ __launch_bounds__(256) void k_route_bwd(RouteBwdLaunch a) {
+  constexpr int GROUPS = 256 / L, EP = L * V;
+  __shared__ float row_lds[GROUPS][EP];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  float* row = row_lds[group];
+  float dp0[V];
+  const int total = a.offsets[a.E], live_n = *a.live;
+  const float g = total > 0 && live_n > 0 ? *a.dloss * (float)a.E / ((float)total * (float)live_n) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = j * L + lane;
+    dp0[j] = e < a.E ? g * (float)(a.offsets[e + 1] - a.offsets[e]) : 0.0f;
+    row[e] = 0.0f;
+  }
+  wave_fence();
+  for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+    const int64_t t = t0 + group;
+    const bool in = t < a.T && (!a.mask || a.mask[t]);
+    float x[V];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * L + lane;
+      x[j] = in && e < a.E ? logit_at<DT>(a.logits, t * a.ld + e) : -__builtin_inff();
+      top = fmaxf(top, x[j]);
+    }
+    int sel = -1;
+    float dw = 0.0f, w = 0.0f;
+    if (in && lane < a.k) {
+      sel = a.indices[t * a.k + lane];
+      if (sel >= a.E) sel = -1;
+      if (sel >= 0) {
+        dw = a.dweights[t * a.k + lane];
+        w = a.weights[t * a.k + lane];
+      }
+    }
+    top = group_reduce<L>(top, [](float p, float q) { return fmaxf(p, q); });
+    const bool live = top > -__builtin_inff();
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int e = j * L + lane;
+      x[j] = live && e < a.E ? __expf(x[j] - top) : 0.0f;
+      sum += x[j];
+    }
+    sum = group_sum<L>(sum);
+    const float inv = live ? 1.0f / sum : 0.0f;
+    float add = dw;
+    if (a.renorm) add = w * (dw - group_sum<L>(w * dw));
+    if (sel >= 0) row[sel] = add;
+    wave_fence();
+    float sc[V], dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      sc[j] = row[j * L + lane];
+      x[j] *= inv;
+      dot = __builtin_fmaf(x[j], a.renorm ? dp0[j] : dp0[j] + sc[j], dot);
+    }
+    dot = group_sum<L>(dot);
+    wave_fence();
+    if (sel >= 0) row[sel] = 0.0f;
+    wave_fence();
+    if (t < a.T) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = j * L + lane;
+        float d = a.renorm ? __builtin_fmaf(x[j], dp0[j] - dot, sc[j]) : x[j] * (dp0[j] + sc[j] - dot);
+        if (!live) d = 0.0f;
+        if (e < a.E) {
+          if constexpr (DT == RT_F32)
+            ((float*)a.dlogits)[t * a.ldd + e] = d;
+          else
+            ((uint16_t*)a.dlogits)[t * a.ldd + e] = (uint16_t)to_bits<DT>(d);
+        }
+      }
+    }
+  }
+}
+
+// lanes per token and experts per lane: 16 lanes up to 256 experts, then 64
+#define GMI_ROUTE_V(KER, DT, E, grid, wg, stream, ...)                                              \
+  do {                                                                                              \
+    if ((E) <= 64) hipLaunchKernelGGL((KER<DT, 16, 4>), dim3(grid), dim3(wg), 0, stream, __VA_ARGS__);       \
+    else if ((E) <= 128) hipLaunchKernelGGL((KER<DT, 16, 8>), dim3(grid), dim3(wg), 0, stream, __VA_ARGS__); \
+    else if ((E) <= 256) hipLaunchKernelGGL((KER<DT, 16, 16>), dim3(grid), dim3(wg), 0, stream, __VA_ARGS__); \
+    else if ((E) <= 512) hipLaunchKernelGGL((KER<DT, 64, 8>), dim3(grid), dim3(wg), 0, stream, __VA_ARGS__); \
+    else hipLaunchKernelGGL((KER<DT, 64, 16>), dim3(grid), dim3(wg), 0, stream, __VA_ARGS__);       \
+  } while (0)
+#define GMI_ROUTE(KER, dtype, E, grid, wg, stream, ...)                                  \
+  do {                                                                                   \
+    if ((dtype) == DT_F16) GMI_ROUTE_V(KER, DT_F16, E, grid, wg, stream, __VA_ARGS__);   \
+    else if ((dtype) == DT_BF16) GMI_ROUTE_V(KER, DT_BF16, E, grid, wg, stream, __VA_ARGS__); \
+    else GMI_ROUTE_V(KER, RT_F32, E, grid, wg, stream, __VA_ARGS__);                     \
+  } while (0)
+
+RoutePlan plan_route(int T, int E) {
+  RoutePlan p;
+  const int64_t passes = ((int64_t)T + RT_PASS - 1) / RT_PASS;
+  // at most 256 workgroups: the second launch reads every workgroup's counts
+  // (one workgroup for no tokens at all: it writes the zero counts)
+  const int64_t per = passes > 256 ? (passes + 255) / 256 : 1;
+  p.tokens_per_wg = (int)(per * RT_PASS);
+  p.wgs = passes > 0 ? (int)((passes + per - 1) / per) : 1;
+  p.bytes = p.wgs > 1 ? (size_t)p.wgs * ((size_t)E * 8 + 4) : 0;
+  return p;
+}
+
+hipError_t launch_route(const RouteLaunch& args, int dtype, void* workspace, hipStream_t stream) {
+  RouteLaunch a = args;
+  const RoutePlan p = plan_route(a.T, a.E);
+  a.tokens_per_wg = p.tokens_per_wg;
+  if (p.wgs > 1) {
+    a.wg_counts = (int32_t*)workspace;
+    a.wg_psum = (float*)(a.wg_counts + (size_t)p.wgs * a.E);
+    a.wg_live = (int32_t*)(a.wg_psum + (size_t)p.wgs * a.E);
+  }
+  GMI_ROUTE(k_route, dtype, a.E, p.wgs, RT_THREADS, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.wgs == 1) return e;
+  hipLaunchKernelGGL(k_route_place, dim3(p.wgs + 1), dim3(RT_THREADS), 0, stream, a, p.wgs);
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(const RouteBwdLaunch& a, int dtype, hipStream_t stream) {
+  const int groups = a.E <= 256 ? 16 : 4;
+  const int64_t need = ((int64_t)a.T + groups - 1) / groups, most = 4 * (int64_t)device_cu_count();
+  const unsigned grid = (unsigned)(need < most ? need : most);
+  GMI_ROUTE(k_route_bwd, dtype, a.E, grid, 256, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace gmi

@@ -58,7 +58,7 @@ typedef enum {
  * instruction, then accumulated in fp32.  This is the fp8 grouped GEMM the
  * element-type aliases of the grouped kernel page admit, on gfx950's
  * v_mfma_scale_f32_32x32x64_f8f6f4 with unit block scales. */
-typedef enum { GMI_F16 = 0, GMI_BF16 = 1, GMI_F8E4M3 = 2 } gmi_dtype;
+typedef enum { GMI_F16 = 0, GMI_BF16 = 1, GMI_F8E4M3 = 2, GMI_F32 = 3 /* routing logits only */ } gmi_dtype;
 
 /* One problem of a grouped GEMM (host memory; the pointers are device
  * pointers).  Mirrors the per-group problem shape (M, N, K) and the per-group
@@ -400,6 +400,146 @@ gmi_status gmi_conv2d_dgrad_implicit(int32_t N, int32_t H, int32_t W, int32_t C,
                                      int32_t dil_h, int32_t dil_w, const void* dy, const void* w, const void* c_in,
                                      void* dx, gmi_dtype dtype, float alpha, float beta, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled fp8 mixture-of-experts layer: a norm that leaves fp8 operands
+ * with scales, the router whose row offsets the grouped calls take, and the
+ * GEMM over block-scaled operands.
+ *
+ * Block scales.  An activation row [K] in fp8 E4M3 carries one fp32 scale per
+ * 128 columns, ceil(K / 128) of them, row-major; a weight [N][K] carries one
+ * per 128 x 128 block, [ceil(N / 128)][ceil(K / 128)].  The last block of a
+ * row or column may be partial.  An element's value is its code times its
+ * block's scale.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm with the residual's addition and an fp8 output:
+ *   h = x + residual              (fp32; written rounded to `dtype` if h is given)
+ *   v = weight * h / sqrt(mean(h^2) + eps)         (from the unrounded h, fp32)
+ *   y = RN(v)                     (if y is given; `dtype`)
+ *   s = max(max |v| over the 128-column block, 448 * 2^-126) / 448
+ *   q = e4m3(v / s)               (if q is given, with scales; nearest even)
+ * One launch, each input read once.  A row that holds a NaN or an infinity
+ * (or whose sum of squares passes the fp32 range) follows fp32 arithmetic.
+ *   rows      >= 0 (0 is a no-op); K in 1 .. 32768, a multiple of 8.
+ *   x         [rows][ldx]; residual [rows][ldr] or NULL (then h = x).
+ *   weight    [K], the type of x, 16-byte aligned.
+ *   eps       finite, >= 0.
+ *   dtype     GMI_F16 or GMI_BF16.
+ *   h, y      [rows][ldh], [rows][ldy] or NULL.
+ *   q         fp8 [rows][ldq], ldq a multiple of 8 (16 where a GEMM call reads
+ *             it), 8-byte aligned; with scales fp32 [rows][lds], lds >=
+ *             ceil(K / 128).  Both or neither; one of y and q at least.
+ * h may be x or residual exactly (same pointer and leading dimension). */
+gmi_status gmi_rmsnorm_quant(int32_t rows, int32_t K, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                             const void* weight, float eps, gmi_dtype dtype, void* h, int64_t ldh, void* y,
+                             int64_t ldy, void* q, int64_t ldq, float* scales, int64_t lds, void* stream);
+
+/* Bytes of the workspace gmi_rmsnorm_bwd needs on the current device when
+ * dweight is wanted; 0 for a non-positive size. */
+size_t gmi_rmsnorm_bwd_workspace_bytes(int32_t rows, int32_t K);
+
+/* Gradients of gmi_rmsnorm_quant's norm.  With r = 1 / sqrt(mean(h^2) + eps),
+ * n = h r and g = weight * dy:
+ *   dh = dres + r (g - n mean(g n))      the gradient of x and of residual alike
+ *   dweight[k] = sum over rows of dy n   fp32, summed in a fixed order
+ * The rounding to fp8 (or to 16 bits) has no derivative of its own: dy is the
+ * gradient of v.
+ *   dy, h     [rows][lddy], [rows][ldh], `dtype`; h as the forward wrote it.
+ *   dres      [rows][lddr], the gradient that reaches h past the norm, or NULL.
+ *   dh        [rows][lddh], `dtype`; may be dy, dres or h exactly.
+ *   dweight   fp32 [K] or NULL; rows == 0 writes zeros.
+ *   workspace needed with dweight: gmi_rmsnorm_bwd_workspace_bytes(rows, K),
+ *             16-byte aligned, scratch.
+ * Sizes, types and alignment as for gmi_rmsnorm_quant. */
+gmi_status gmi_rmsnorm_bwd(int32_t rows, int32_t K, const void* dy, int64_t lddy, const void* h, int64_t ldh,
+                           const void* weight, const void* dres, int64_t lddr, float eps, gmi_dtype dtype, void* dh,
+                           int64_t lddh, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of the optional workspace that lets gmi_gemm_f8_block split K for this
+ * shape on the current device; 0 when no split is used. */
+size_t gmi_gemm_f8_block_workspace_bytes(int32_t M, int32_t N, int32_t K);
+
+/* Block-scaled fp8 GEMM:
+ *   Y[m][n] = RN_bf16( sum_b x_scales[m][b] * w_scales[n / 128][b] * sum_{k in block b} X[m][k] W[n][k] )
+ * The sum inside a block of 128 k is the matrix instruction's (exact products,
+ * fp32 sums); blocks are scaled and added in fp32.  With the transposed weight
+ * [K][N] and transposed scales it is the data gradient, dY in the place of X.
+ *   X         fp8 E4M3 [M][ldx]; x_scales fp32 [M][ldxs], ldxs >= ceil(K / 128).
+ *   W         fp8 E4M3 [N][ldw]; w_scales fp32 [ceil(N / 128)][ldws].
+ *   Y         bf16 [M][ldy], ldy a multiple of 8.
+ *   workspace optional: with gmi_gemm_f8_block_workspace_bytes(M, N, K) bytes,
+ *             16-byte aligned, shapes whose tiles cannot fill the device split
+ *             K (fp32 partials, summed in order by a second launch); NULL or
+ *             smaller runs unsplit.
+ * K, ldx and ldw multiples of 16, else GMI_ERR_UNSUPPORTED; N and M are free.
+ * M == 0 or N == 0 is a no-op; K == 0 gives zeros. */
+gmi_status gmi_gemm_f8_block(int32_t M, int32_t N, int32_t K, const void* X, int64_t ldx, const float* x_scales,
+                             int64_t ldxs, const void* W, int64_t ldw, const float* w_scales, int64_t ldws, void* Y,
+                             int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace gmi_gemm_f8_block_grouped needs for `count` groups. */
+size_t gmi_gemm_f8_block_grouped_workspace_bytes(int32_t count);
+
+/* The same per group, the group sizes on the device (as for
+ * gmi_gemm_grouped_offsets): group g owns rows [offsets[g], offsets[g + 1]) of
+ * X, x_scales and Y, clipped to [0, rows), and multiplies them by
+ *   W_g = W + g * w_stride (bytes), w_scales_g = w_scales + g * ws_stride (floats).
+ *   count     0 .. 1024 groups.
+ *   strides   at least one group's data when count > 1; w_stride a multiple of 16.
+ *   workspace at least gmi_gemm_f8_block_grouped_workspace_bytes(count) bytes,
+ *             16-byte aligned.
+ * Rows outside every group are not written; K == 0 gives zeros. */
+gmi_status gmi_gemm_f8_block_grouped(int32_t count, const int32_t* offsets, int32_t rows, int32_t N, int32_t K,
+                                     const void* X, int64_t ldx, const float* x_scales, int64_t ldxs, const void* W,
+                                     int64_t ldw, int64_t w_stride, const float* w_scales, int64_t ldws,
+                                     int64_t ws_stride, void* Y, int64_t ldy, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Bytes of the workspace gmi_moe_route needs for this size (0 for up to 64
+ * tokens). */
+size_t gmi_moe_route_workspace_bytes(int32_t tokens, int32_t experts);
+
+/* Expert routing.  A token is live if the mask keeps it and one of its logits
+ * lies above -infinity.  p = softmax(logits) of a live token.
+ *   indices[t][i]  the expert of the i-th largest logit (equal logits: lowest
+ *                  expert first); -1 where no logit above -infinity is left
+ *                  and for tokens that are not live.  A NaN is never taken.
+ *   weights[t][i]  p at that expert, divided by the token's sum of them if
+ *                  `renormalize`; 0 with index -1.
+ *   counts[e], offsets[e], offsets[E]
+ *                  slots (t, i) per expert, their exclusive sums, the total:
+ *                  the row offsets of the grouped calls.
+ *   slot_row[t][i] the row of a slot when slots are ordered by expert, inside
+ *                  an expert by token; -1 with index -1.
+ *   row_slot[r]    the slot t * k + i of row r; -1 from offsets[E] on.
+ *   loss           E * sum_e (counts[e] / offsets[E]) * mean over live tokens of p_e;
+ *                  0 without live tokens.
+ *   live           live tokens.
+ * A NaN or +infinity among a live token's logits makes its weights and the
+ * loss NaN.  Every result is the same on every run.
+ *   tokens    >= 0, tokens * k < 2^31; experts 1 .. 1024; k 1 .. min(16, experts).
+ *   logits    [tokens][ld], dtype GMI_F16, GMI_BF16 or GMI_F32, ld >= experts.
+ *   mask      bytes [tokens], 0 for tokens left out; NULL keeps all.
+ *   workspace gmi_moe_route_workspace_bytes(tokens, experts) bytes, 4-byte
+ *             aligned; may be NULL when that is 0. */
+gmi_status gmi_moe_route(int32_t tokens, int32_t experts, int32_t k, const void* logits, int64_t ld, gmi_dtype dtype,
+                         const uint8_t* mask, int32_t renormalize, int32_t* indices, float* weights, int32_t* counts,
+                         int32_t* offsets, int32_t* slot_row, int32_t* row_slot, float* loss, int32_t* live,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the logits from that of the weights (dweights [tokens][k]) and
+ * of the loss (dloss, one float on the device), with what gmi_moe_route wrote:
+ *   dp_e = dloss * E * (counts[e] / offsets[E]) / live  (+ dweights at the taken experts without renormalize)
+ *   dlogits_e = p_e (dp_e - sum_f p_f dp_f)
+ * and with renormalize the taken experts' w_i (dweights_i - sum_j w_j dweights_j)
+ * on top.  Counts are constants (they have no derivative); dweights of slots
+ * without an expert are not read; tokens that are not live get zeros.
+ *   dlogits   [tokens][ldd], the type of logits. */
+gmi_status gmi_moe_route_bwd(int32_t tokens, int32_t experts, int32_t k, const void* logits, int64_t ld,
+                             gmi_dtype dtype, const uint8_t* mask, int32_t renormalize, const int32_t* indices,
+                             const float* weights, const int32_t* offsets, const int32_t* live,
+                             const float* dweights, const float* dloss, void* dlogits, int64_t ldd, void* stream);
 
 /* Text of the last failed check or HIP error on the calling thread ("" if
  * none).  The pointer stays valid until the next gmi_* call on that thread. */

@@ -1,0 +1,164 @@
+"""GPU: block-scaled fp8 GEMM, dense and per group, against float64 on the
+decoded operands (tolerance: moe_ref.gemm_tolerance)."""
+import pytest
+import torch
+
+import moe_ref as ref
+from helpers import SENTINEL, dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gmi():
+    import grouped_mixed_input_amd as g
+
+    g.lib()
+    return g
+
+
+def _codes(gen, *shape):
+    return (torch.randn(*shape, generator=gen) * 100).clamp(-448, 448).to(ref.F8)
+
+
+def _scales(gen, *shape):
+    return torch.exp(0.5 * torch.randn(*shape, generator=gen)) * 0.01
+
+
+def _padded(t, ld, fill):
+    """`t` on the device with leading dimension ld, the padding holding `fill` (NaN codes must never be read)."""
+    buf = torch.empty(*t.shape[:-1], ld, dtype=t.dtype)
+    if t.dtype == ref.F8:
+        buf.view(torch.uint8).fill_(0x7F)
+    else:
+        buf.fill_(fill)
+    buf[..., : t.shape[-1]] = t
+    return buf.to(dev())[..., : t.shape[-1]]
+
+
+def _out(rows, N, ld):
+    return torch.full((rows, ld), SENTINEL, dtype=torch.int16, device=dev()).view(torch.bfloat16)[:, :N]
+
+
+def _assert_close(Y, X, xs, W, ws, what):
+    r, mag = ref.gemm(X, xs, W, ws)
+    err = (Y.cpu().double() - r).abs()
+    bad = ~(err <= ref.gemm_tolerance(r, mag, X.shape[1]))
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
+
+
+SHAPES = [(1, 1, 16), (1, 128, 128), (2, 37, 144), (16, 256, 2048), (15, 130, 1040), (17, 96, 272), (33, 200, 512),
+          (64, 384, 128), (65, 257, 400), (100, 1000, 1040), (130, 300, 272), (257, 129, 512), (300, 520, 1152),
+          (513, 1024, 256), (1000, 777, 128), (8, 4096, 4096)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("split", [False, True])
+def test_dense_shapes(gmi, M, N, K, split):
+    gen = torch.Generator().manual_seed(M * 31 + N + K)
+    X, W = _codes(gen, M, K), _codes(gen, N, K)
+    xs, ws = _scales(gen, M, ref.blocks(K)), _scales(gen, ref.blocks(N), ref.blocks(K))
+    ldy = (N + 7) // 8 * 8 + 8
+    Y = _out(M, N, ldy)
+    gmi.gemm_f8_block(_padded(X, K + 32, 0), _padded(xs, ref.blocks(K) + 3, float("nan")), _padded(W, K + 16, 0),
+                      _padded(ws, ref.blocks(K) + 1, float("nan")), Y=Y,
+                      workspace=None if split else torch.empty(0, dtype=torch.uint8, device=dev()))
+    torch.cuda.synchronize()
+    _assert_close(Y, X, xs, W, ws, f"dense {M}x{N}x{K}")
+    assert (Y._base.view(torch.int16)[:, N:] == SENTINEL).all(), "padding columns written"
+
+
+@pytest.mark.parametrize("M,N,K", [(2048, 2176, 1040), (4100, 2048, 384), (2304, 4000, 256)])
+def test_dense_large_tiles(gmi, M, N, K):
+    gen = torch.Generator().manual_seed(M + N + K)
+    X, W = _codes(gen, M, K), _codes(gen, N, K)
+    xs, ws = _scales(gen, M, ref.blocks(K)), _scales(gen, ref.blocks(N), ref.blocks(K))
+    Y = gmi.gemm_f8_block(X.to(dev()), xs.to(dev()), W.to(dev()), ws.to(dev()))
+    torch.cuda.synchronize()
+    rows = torch.cat([torch.arange(0, M, 37), torch.arange(M - 3, M)])
+    _assert_close(Y[rows.to(dev())], X[rows], xs[rows], W, ws, f"dense {M}x{N}x{K}")
+
+
+def test_integer_operands_are_exact(gmi):
+    # codes in {-2 .. 2}, scales powers of two: every partial sum is exact in fp32, the result below 2^8 in bf16
+    gen = torch.Generator().manual_seed(5)
+    for M, N, K in [(20, 160, 64), (300, 300, 64), (2100, 2100, 32)]:
+        X = torch.randint(-2, 3, (M, K), generator=gen).float().to(ref.F8)
+        W = torch.randint(-2, 3, (N, K), generator=gen).float().to(ref.F8)
+        xs = torch.pow(2.0, torch.randint(-3, 4, (M, 1), generator=gen).float())
+        ws = torch.pow(2.0, torch.randint(-3, 4, (ref.blocks(N), 1), generator=gen).float())
+        Y = gmi.gemm_f8_block(X.to(dev()), xs.to(dev()), W.to(dev()), ws.to(dev()))
+        r, _ = ref.gemm(X, xs, W, ws)
+        assert torch.equal(Y.cpu(), r.to(torch.bfloat16))
+
+
+def test_empty_sizes(gmi):
+    X0 = torch.empty(4, 0, dtype=torch.uint8, device=dev()).view(ref.F8)
+    Y = _out(4, 5, 8)
+    gmi.gemm_f8_block(X0, torch.empty(4, 0, device=dev()), X0.new_empty(5, 0), torch.empty(1, 0, device=dev()), Y=Y)
+    assert (Y == 0).all()
+    none = torch.empty(0, 32, dtype=torch.uint8, device=dev()).view(ref.F8)
+    W = torch.zeros(8, 32, dtype=torch.uint8, device=dev()).view(ref.F8)
+    assert gmi.gemm_f8_block(none, torch.empty(0, 1, device=dev()), W, torch.ones(1, 1, device=dev())).shape == (0, 8)
+
+
+def test_transposed_weight_gives_the_data_gradient(gmi):
+    gen = torch.Generator().manual_seed(8)
+    M, N, K = 70, 256, 384
+    dY, W = _codes(gen, M, N), _codes(gen, N, K)
+    ds, ws = _scales(gen, M, ref.blocks(N)), _scales(gen, ref.blocks(N), ref.blocks(K))
+    Wt = W.view(torch.uint8).t().contiguous().view(ref.F8)
+    dX = gmi.gemm_f8_block(dY.to(dev()), ds.to(dev()), Wt.to(dev()), ws.t().contiguous().to(dev()))
+    want = ref.spread(dY, ds, 1) @ ref.spread(W, ws, 128)
+    mag = ref.spread(dY, ds, 1).abs() @ ref.spread(W, ws, 128).abs()
+    assert ((dX.cpu().double() - want).abs() <= ref.gemm_tolerance(want, mag, N)).all()
+
+
+def _grouped(gmi, counts, N, K, seed, spare=3, first=0):
+    gen = torch.Generator().manual_seed(seed)
+    rows, G = first + sum(counts) + spare, len(counts)
+    X, W = _codes(gen, rows, K), _codes(gen, G, N, K)
+    xs, ws = _scales(gen, rows, ref.blocks(K)), _scales(gen, G, ref.blocks(N), ref.blocks(K))
+    off = [first]
+    for c in counts:
+        off.append(off[-1] + c)
+    Y = _out(rows, N, (N + 7) // 8 * 8)
+    gmi.gemm_f8_block_grouped(torch.tensor(off, dtype=torch.int32, device=dev()), X.to(dev()), xs.to(dev()),
+                              W.to(dev()), ws.to(dev()), Y=Y)
+    torch.cuda.synchronize()
+    for g, c in enumerate(counts):
+        if c:
+            s = slice(off[g], off[g + 1])
+            _assert_close(Y[s], X[s], xs[s], W[g], ws[g], f"group {g} of {c} rows")
+    raw = Y._base.view(torch.int16)
+    assert (raw[:first] == SENTINEL).all() and (raw[off[-1]:] == SENTINEL).all(), "rows outside every group written"
+
+
+@pytest.mark.parametrize("N,K", [(128, 128), (200, 272), (520, 1040)])
+def test_grouped_mixed_sizes(gmi, N, K):
+    _grouped(gmi, [0, 1, 2, 15, 16, 17, 0, 31, 32, 33, 63, 64, 65, 100, 128, 129, 200, 256, 257, 300, 0], N, K, N + K,
+             first=2)
+
+
+def test_grouped_few_rows(gmi):
+    _grouped(gmi, [1, 0, 3, 0, 2, 1, 0, 9], 384, 512, 1, spare=0)
+    _grouped(gmi, [7], 130, 144, 2)
+
+
+def test_grouped_many_groups(gmi):
+    _grouped(gmi, [(7 * g) % 23 for g in range(1024)], 64, 128, 4)
+
+
+def test_grouped_bad_offsets_stay_inside(gmi):
+    # reversed, negative and oversized ranges are clipped: nothing outside [0, rows) is touched
+    gen = torch.Generator().manual_seed(6)
+    rows, N, K = 300, 128, 128
+    X, W = _codes(gen, rows, K), _codes(gen, 4, N, K)
+    xs, ws = _scales(gen, rows, 1), _scales(gen, 4, 1, 1)
+    buf = torch.full((rows + 512, N), SENTINEL, dtype=torch.int16, device=dev())
+    Y = buf[256: 256 + rows].view(torch.bfloat16)
+    off = torch.tensor([-50, 40, 20, 250, 100000], dtype=torch.int32, device=dev())
+    gmi.gemm_f8_block_grouped(off, X.to(dev()), xs.to(dev()), W.to(dev()), ws.to(dev()), Y=Y)
+    torch.cuda.synchronize()
+    assert (buf[:256] == SENTINEL).all() and (buf[256 + rows:] == SENTINEL).all()
+    _assert_close(Y[250:], X[250:], xs[250:], W[3], ws[3], "the clipped last group")
