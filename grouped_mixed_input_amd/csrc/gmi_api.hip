@@ -857,6 +857,9 @@ gmi_status gmi_rmsnorm_bwd(int32_t rows, int32_t K, const void* dy, int64_t lddy
   return hip_status(launch_rmsnorm_bwd(a, (int)dtype, dweight, (hipStream_t)stream), who);
 }
 
+// a launch's threads stay below 2^32
+constexpr int64_t kMaxF8Tiles = int64_t(1) << 22;
+
 // Checks shared by the block-scaled GEMM calls and the launch record they
 // fill; `nothing` is set when there is no work.
 static gmi_status f8_block_prepare(const char* who, int32_t M, int32_t N, int32_t K, const void* X, int64_t ldx,
@@ -874,6 +877,10 @@ static gmi_status f8_block_prepare(const char* who, int32_t M, int32_t N, int32_
     return fail(GMI_ERR_INVALID_ARG, "%s: a leading dimension below its row width", who);
   if (ldy > kMaxLd || (K > 0 && (ldx > kMaxLd || ldw > kMaxLd || ldxs > kMaxLd || ldws > kMaxLd)))
     return fail(GMI_ERR_UNSUPPORTED, "%s: a leading dimension above 2^22 elements", who);
+  if (K > 0 && ldxs > kMaxLd / 4)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: ldxs above 2^20 elements", who);
+  if (cdiv(M, 256) * cdiv(N, 256) > kMaxF8Tiles)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: more than 2^22 output tiles of 256 x 256", who);
   if (K % 16 || (K > 0 && (ldx % 16 || ldw % 16)))
     return fail(GMI_ERR_UNSUPPORTED, "%s: fp8 needs K, ldx and ldw multiples of 16", who);
   if (!aligned16(Y) || ldy % 8 ||
