@@ -903,6 +903,9 @@ static gmi_status f8_block_prepare(const char* who, int32_t M, int32_t N, int32_
   a.offsets = nullptr;
   a.count = 0;
   a.w_stride = a.ws_stride = 0;
+  a.splits = 1;
+  a.part = nullptr;
+  a.ldp = 0;
   return GMI_OK;
 }
 
@@ -952,6 +955,9 @@ gmi_status gmi_gemm_f8_block_grouped(int32_t count, const int32_t* offsets, int3
   if (K > 0 && count > 1 &&
       (w_stride < (int64_t)(N - 1) * ldw + K || ws_stride < (cdiv(N, 128) - 1) * ldws + cdiv(K, 128)))
     return fail(GMI_ERR_INVALID_ARG, "%s: a group stride is smaller than one group's data", who);
+  // every group may add a partial tile
+  if ((rows / 256 + (int64_t)std::min(count, rows)) * cdiv(N, 256) > kMaxF8Tiles)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: may need more than 2^22 output tiles of 256 x 256", who);
   if (w_stride % 16) return fail(GMI_ERR_MISALIGNED, "%s: w_stride must be a multiple of 16", who);
   const size_t need = f8_block_grouped_workspace(count);
   if (!workspace || workspace_bytes < need)

@@ -151,6 +151,9 @@ __device__ __forceinline__ uint32_t buf_load1(rsrc_t r, uint32_t off) {
 }
 // as above, with a wave-uniform byte offset soff (an SGPR) added to the lane
 // offset; a lane at OOB stays past the resource for any soff below 2^31
+__device__ __forceinline__ u32x4 buf_load16s(rsrc_t r, uint32_t off, uint32_t soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, (int)soff, 0));
+}
 __device__ __forceinline__ u32x2 buf_load8s(rsrc_t r, uint32_t off, uint32_t soff) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, (int)soff, 0));
 }

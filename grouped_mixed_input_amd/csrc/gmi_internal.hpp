@@ -211,6 +211,9 @@ struct F8BlockLaunch {
   const int32_t* offsets;  // grouped: count + 1 row offsets on the device
   int count;
   int64_t w_stride, ws_stride;
+  int splits;   // dense: runs of K, each with its fp32 sums in `part` (NULL without a split)
+  float* part;  // [splits][M][ldp]
+  int64_t ldp;
 };
 size_t f8_block_workspace(int M, int N, int K);   // of the split over K; 0 without one
 size_t f8_block_grouped_workspace(int count);     // the group table

@@ -40,10 +40,22 @@ def _out(rows, N, ld):
     return torch.full((rows, ld), SENTINEL, dtype=torch.int16, device=dev()).view(torch.bfloat16)[:, :N]
 
 
-def _assert_close(Y, X, xs, W, ws, what):
+def _lost_products(X, xs, W, ws):
+    """What the fp8 matrix instruction may drop: it brings the products it adds at a time to the exponent of their
+    largest and keeps 13 bits below it, so each loses less than 2^-13 of the largest (bounded here by the block's
+    largest factors)."""
+    out = 0.0
+    for b in range(ref.blocks(X.shape[1])):
+        x, w = X[:, 128 * b: 128 * b + 128].double().abs(), W[:, 128 * b: 128 * b + 128].double().abs()
+        top = (x.amax(1) * xs[:, b].double())[:, None] * (w.amax(1) * ws[:, b].double().repeat_interleave(128)[: len(w)])
+        out = out + x.shape[1] * 2.0 ** -13 * top
+    return out
+
+
+def _assert_close(Y, X, xs, W, ws, what, lost=None):
     r, mag = ref.gemm(X, xs, W, ws)
     err = (Y.cpu().double() - r).abs()
-    bad = ~(err <= ref.gemm_tolerance(r, mag, X.shape[1]))
+    bad = ~(err <= ref.gemm_tolerance(r, mag, X.shape[1]) + (0.0 if lost is None else lost(X, xs, W, ws)))
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
 
 
@@ -114,7 +126,7 @@ def test_transposed_weight_gives_the_data_gradient(gmi):
     assert ((dX.cpu().double() - want).abs() <= ref.gemm_tolerance(want, mag, N)).all()
 
 
-def _grouped(gmi, counts, N, K, seed, spare=3, first=0):
+def _grouped(gmi, counts, N, K, seed, spare=3, first=0, lost=None):
     gen = torch.Generator().manual_seed(seed)
     rows, G = first + sum(counts) + spare, len(counts)
     X, W = _codes(gen, rows, K), _codes(gen, G, N, K)
@@ -129,7 +141,7 @@ def _grouped(gmi, counts, N, K, seed, spare=3, first=0):
     for g, c in enumerate(counts):
         if c:
             s = slice(off[g], off[g + 1])
-            _assert_close(Y[s], X[s], xs[s], W[g], ws[g], f"group {g} of {c} rows")
+            _assert_close(Y[s], X[s], xs[s], W[g], ws[g], f"group {g} of {c} rows", lost)
     raw = Y._base.view(torch.int16)
     assert (raw[:first] == SENTINEL).all() and (raw[off[-1]:] == SENTINEL).all(), "rows outside every group written"
 
@@ -162,3 +174,52 @@ def test_grouped_bad_offsets_stay_inside(gmi):
     torch.cuda.synchronize()
     assert (buf[:256] == SENTINEL).all() and (buf[256 + rows:] == SENTINEL).all()
     _assert_close(Y[250:], X[250:], xs[250:], W[3], ws[3], "the clipped last group")
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 200, 4112), (130, 520, 8192), (40, 72, 8192), (9, 1000, 8080)])
+def test_dense_split_over_k(gmi, M, N, K):
+    # few tiles and a long K: the sums of the splits are joined by a second launch, also at ragged ends
+    assert gmi.lib().gmi_gemm_f8_block_workspace_bytes(M, N, K) > 0
+    gen = torch.Generator().manual_seed(M + N + K)
+    X, W = _codes(gen, M, K), _codes(gen, N, K)
+    xs, ws = _scales(gen, M, ref.blocks(K)), _scales(gen, ref.blocks(N), ref.blocks(K))
+    outs = []
+    for work in (None, torch.empty(0, dtype=torch.uint8, device=dev())):
+        Y = _out(M, N, (N + 7) // 8 * 8 + 8)
+        args = [t.to(dev()) for t in (X, xs, W, ws)]
+        gmi.gemm_f8_block(*args, Y=Y, workspace=work)
+        torch.cuda.synchronize()
+        _assert_close(Y, X, xs, W, ws, f"split {work is None} {M}x{N}x{K}", _lost_products)
+        assert (Y._base.view(torch.int16)[:, N:] == SENTINEL).all(), "padding columns written"
+        again = _out(M, N, (N + 7) // 8 * 8 + 8)
+        gmi.gemm_f8_block(*args, Y=again, workspace=work)
+        assert torch.equal(again.view(torch.int16), Y.view(torch.int16))
+        outs.append(Y)
+
+
+@pytest.mark.parametrize("K", [16, 128, 144, 256, 384, 400, 512, 640, 1024, 1152, 1536])
+def test_grouped_every_row_class_and_block_count(gmi, K):
+    # 1 to 12 k-blocks (rings shorter and longer than K, rotated starts), rows on both sides of each tile shape
+    _grouped(gmi, [130, 1, 64, 65, 128, 129, 0, 256, 257, 321, 385, 513, 20], 260, K, K, first=1,
+             lost=_lost_products)
+
+
+def test_row_scales_that_are_zero_or_not_finite_stay_in_their_rows(gmi):
+    gen = torch.Generator().manual_seed(17)
+    for M, counts in ((100, None), (8, None), (600, [100, 60, 300, 140])):
+        N, K = 136, 640
+        X, xs = _codes(gen, M, K), _scales(gen, M, 5)
+        xs[2, 1], xs[3, 0], xs[5] = float("nan"), float("inf"), 0.0
+        if counts is None:
+            W, ws = _codes(gen, N, K), _scales(gen, 2, 5)
+            Y = gmi.gemm_f8_block(X.to(dev()), xs.to(dev()), W.to(dev()), ws.to(dev()))
+        else:
+            W, ws = _codes(gen, 4, N, K), _scales(gen, 4, 2, 5)
+            off = torch.tensor([0, 100, 160, 460, 600], dtype=torch.int32, device=dev())
+            Y = gmi.gemm_f8_block_grouped(off, X.to(dev()), xs.to(dev()), W.to(dev()), ws.to(dev()))
+            W, ws = W[0], ws[0]
+        Y = Y.cpu()
+        assert torch.isnan(Y[2]).all() and not torch.isfinite(Y[3]).any() and (Y[5] == 0).all()
+        keep = torch.tensor([i for i in range(8) if i not in (2, 3)])
+        _assert_close(Y[keep], X[keep], xs[keep], W, ws, "the other rows", _lost_products)
+        assert torch.isfinite(Y[6:]).all()
