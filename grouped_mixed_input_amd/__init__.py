@@ -129,8 +129,8 @@ def _check(status: int) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -431,18 +431,19 @@ def _scratch(workspace, need: int, device, stream):
 
 def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype) -> int:
     """Checks a device matrix with unit stride along its rows; returns its leading dimension."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.dtype is not dtype or t.shape != (rows, cols):
         raise ValueError(f"{name} must be {dtype} [{rows}][{cols}], got {t.dtype} {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the device")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
     # with at most one row the stride says nothing: any legal leading dimension does
-    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    return ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _vector(t: torch.Tensor, name: str, n: int, dtype) -> int:
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device tensor of {n} {dtype}")
     return t.data_ptr()
 
