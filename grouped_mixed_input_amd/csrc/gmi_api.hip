@@ -1013,8 +1013,8 @@ gmi_status gmi_moe_route(int32_t tokens, int32_t experts, int32_t k, const void*
   const size_t need = gmi_moe_route_workspace_bytes(tokens, experts);
   if (need && (!workspace || workspace_bytes < need))
     return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
-  if (need && ((uintptr_t)workspace & 3u))
-    return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 4-byte aligned", who);
+  if (need && !aligned16(workspace))
+    return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
   RouteLaunch a{};
   a.logits = logits;
   a.mask = mask;

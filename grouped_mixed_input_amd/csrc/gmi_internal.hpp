@@ -230,7 +230,8 @@ struct RouteLaunch {
   float *weights, *loss;
   // several workgroups: their counts and sums of p per expert, and live tokens
   int tokens_per_wg;
-  int32_t *wg_counts, *wg_live;
+  uint16_t* wg_counts;
+  int32_t* wg_live;
   float* wg_psum;
 };
 struct RouteBwdLaunch {

@@ -16,6 +16,8 @@
 // Order within an expert: a bitmask per expert over the 64 tokens of a pass
 // gives each slot its rank by counting the bits below it -- no sort, and the
 // same result on every run.
+#include <algorithm>
+
 #include "gmi_device.hpp"
 #include "gmi_internal.hpp"
 
@@ -124,6 +126,8 @@ __device__ __forceinline__ void write_loss(const RouteLaunch& a, float psum, int
   }
 }
 
+// row length of the workgroups' counts and sums: 16-byte loads
+__device__ __forceinline__ int route_ld(int E) { return (E + 7) & ~7; }
 // Routing of a contiguous range of tokens per workgroup.  Writes indices,
 // weights and each slot's rank among the workgroup's slots of its expert
 // (into slot_row), and the workgroup's counts and sums of p per expert.  With
@@ -275,9 +279,10 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
   if (e < a.E)
     for (int i = 0; i < RT_THREADS / 64; ++i) ps += psum_lds[i][e];
   if (gridDim.x > 1) {
-    if (e < a.E) {
-      a.wg_counts[(int64_t)blockIdx.x * a.E + e] = base[e];
-      a.wg_psum[(int64_t)blockIdx.x * a.E + e] = ps;
+    const int ld = route_ld(a.E);
+    if (e < ld) {
+      a.wg_counts[(int64_t)blockIdx.x * ld + e] = (uint16_t)base[e];
+      a.wg_psum[(int64_t)blockIdx.x * ld + e] = ps;
     }
     if (e == 0) a.wg_live[blockIdx.x] = live_wg;
     return;
@@ -307,71 +312,118 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
 
 // Second launch: every workgroup sums the count matrix for itself (totals, and
 // what lies before its own tokens), turns the ranks of its slots into rows and
-// writes both orders.  One further workgroup writes counts, offsets and loss.
+// writes both orders.  One further workgroup writes counts, offsets and loss;
+// it has the longest way and so asks for the sums of p before all else.
+// Latency is what it costs, so the slots are fetched before the matrix, the
+// matrix is 16 bits wide and read eight experts a load: with 256 workgroups and
+// 128 experts four loads a thread (32-bit, one expert a load: 15.9 us).
 __global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int wgs) {
-  __shared__ int tot[RT_THREADS], pre[RT_THREADS], row0[RT_THREADS];
-  __shared__ float ps[RT_THREADS];
+  __shared__ int32_t part[2][8 * RT_THREADS];  // partial totals and prefixes, then floats of the sums of p
+  __shared__ int row0[RT_THREADS];
   __shared__ int wave_i[RT_THREADS / 64];
   __shared__ float wave_f[RT_THREADS / 64];
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, tid = threadIdx.x, ld = route_ld(a.E);
   const bool last = b == wgs;
-  int ep = 1;
-  while (ep < a.E) ep *= 2;
-  const int slices = RT_THREADS / ep, e = threadIdx.x % ep, sl = threadIdx.x / ep;
-  const int per = (wgs + slices - 1) / slices;
-  int st = 0, sp = 0;
-  float sf = 0.0f;
-  if (e < a.E) {
-    const int q1 = min(wgs, (sl + 1) * per);
+  const int64_t s0 = (int64_t)b * a.tokens_per_wg * a.k;
+  const int64_t s1 = last ? s0 : min((int64_t)a.T * a.k, s0 + (int64_t)a.tokens_per_wg * a.k);
+  int x = -1, r = 0;
+  if (s0 + tid < s1) {
+    x = a.indices[s0 + tid];
+    r = a.slot_row[s0 + tid];
+  }
+  // sums of p: a team of `four` threads reads one row, four experts a load
+  int four = 1, live = 0;
+  while (four < ld / 4) four *= 2;
+  const int fc = tid % four;
+  f32x4 ps{};
+  if (last) {
+    if (fc < ld / 4) {
 #pragma unroll 8
-    for (int q = sl * per; q < q1; ++q) {
-      const int c = a.wg_counts[(int64_t)q * a.E + e];
-      st += c;
-      sp += q < b ? c : 0;
-      if (last) sf += a.wg_psum[(int64_t)q * a.E + e];
+      for (int q = tid / four; q < wgs; q += RT_THREADS / four) ps += *(const f32x4*)(a.wg_psum + (int64_t)q * ld + 4 * fc);
+    }
+    for (int q = tid; q < wgs; q += RT_THREADS) live += a.wg_live[q];
+  }
+  // a team of `team` threads (a power of two) reads one row of the matrix
+  int team = 1;
+  while (team < ld / 8) team *= 2;
+  const int slices = RT_THREADS / team, c = tid % team, sl = tid / team;
+  int tot[8], pre[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
+  if (c < ld / 8) {
+#pragma unroll 4
+    for (int q = sl; q < wgs; q += slices) {
+      const u32x4 v = *(const u32x4*)(a.wg_counts + (int64_t)q * ld + 8 * c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = (int)(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xffffu);
+        tot[i] += n;
+        pre[i] += q < b ? n : 0;
+      }
     }
   }
-  tot[threadIdx.x] = st;
-  pre[threadIdx.x] = sp;
-  ps[threadIdx.x] = sf;
+  // the teams of a wave, then the waves (or slices, of teams wider than a wave)
+  for (int d = team; d < 64; d *= 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      tot[i] += __shfl_xor(tot[i], d);
+      pre[i] += __shfl_xor(pre[i], d);
+    }
+  }
+  const int wide = max(team, 64), groups = RT_THREADS / wide;
+  if (tid % wide < team) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[0][(tid / wide) * team * 8 + c * 8 + i] = tot[i];
+      part[1][(tid / wide) * team * 8 + c * 8 + i] = pre[i];
+    }
+  }
   __syncthreads();
-  st = sp = 0;
-  sf = 0.0f;
-  if ((int)threadIdx.x < a.E) {
-    for (int s = 0; s < slices; ++s) {
-      st += tot[s * ep + threadIdx.x];
-      sp += pre[s * ep + threadIdx.x];
-      sf += ps[s * ep + threadIdx.x];
+  int st = 0, sp = 0;
+  if (tid < a.E) {
+    for (int g = 0; g < groups; ++g) {
+      st += part[0][g * team * 8 + tid];
+      sp += part[1][g * team * 8 + tid];
     }
   }
   int total;
   const int off = block_scan(st, wave_i, total);
-  row0[threadIdx.x] = off + sp;
+  row0[tid] = off + sp;
   __syncthreads();
   if (last) {
-    if ((int)threadIdx.x < a.E) {
-      a.counts[threadIdx.x] = st;
-      a.offsets[threadIdx.x] = off;
+    if (tid < a.E) {
+      a.counts[tid] = st;
+      a.offsets[tid] = off;
     }
-    if (threadIdx.x == 0) a.offsets[a.E] = total;
-    int live = 0;
-    for (int q = threadIdx.x; q < wgs; q += RT_THREADS) live += a.wg_live[q];
+    if (tid == 0) a.offsets[a.E] = total;
+    // the lanes of a wave that hold the same experts, then the waves
+    float* fp = (float*)part[0];
+    for (int d = four; d < 64; d *= 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ps[i] += __shfl_xor(ps[i], d);
+    }
+    const int wide4 = max(four, 64);
+    if (tid % wide4 < four) *(f32x4*)(fp + (tid / wide4) * four * 4 + fc * 4) = ps;
     int live_all;
-    __syncthreads();
-    block_scan(live, wave_i, live_all);
+    block_scan(live, wave_i, live_all);  // its barriers publish the sums too
+    float sf = 0.0f;
+    if (tid < a.E)
+      for (int g = 0; g < RT_THREADS / wide4; ++g) sf += fp[g * four * 4 + tid];
     write_loss(a, sf, st, total, live_all, wave_f);
     return;
   }
-  const int64_t s0 = (int64_t)b * a.tokens_per_wg * a.k;
-  const int64_t s1 = min((int64_t)a.T * a.k, s0 + (int64_t)a.tokens_per_wg * a.k);
-  for (int64_t s = s0 + threadIdx.x; s < s1; s += RT_THREADS) {
-    const int x = a.indices[s];
+  for (int64_t s = s0 + tid; s < s1;) {
     if (x >= 0) {
-      const int r = row0[x] + a.slot_row[s];
+      r += row0[x];
       a.slot_row[s] = r;
       a.row_slot[r] = (int)s;
     }
     if (s >= total) a.row_slot[s] = -1;  // rows past the last one; s runs over every row number too
+    s += RT_THREADS;
+    if (s < s1) {
+      x = a.indices[s];
+      r = a.slot_row[s];
+    }
   }
 }
 
@@ -486,12 +538,12 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouteBwdLaunch a) {
 RoutePlan plan_route(int T, int E) {
   RoutePlan p;
   const int64_t passes = ((int64_t)T + RT_PASS - 1) / RT_PASS;
-  // at most 256 workgroups: the second launch reads every workgroup's counts
-  // (one workgroup for no tokens at all: it writes the zero counts)
-  const int64_t per = passes > 256 ? (passes + 255) / 256 : 1;
-  p.tokens_per_wg = (int)(per * RT_PASS);
+  // 256 workgroups: the second launch reads every workgroup's counts, which
+  // have 16 bits (one workgroup for no tokens at all: it writes the zero counts)
+  const int64_t per = std::min<int64_t>((passes + 255) / 256, 65535 / RT_PASS);
+  p.tokens_per_wg = (int)(std::max<int64_t>(per, 1) * RT_PASS);
   p.wgs = passes > 0 ? (int)((passes + per - 1) / per) : 1;
-  p.bytes = p.wgs > 1 ? (size_t)p.wgs * ((size_t)E * 8 + 4) : 0;
+  p.bytes = p.wgs > 1 ? (size_t)p.wgs * ((size_t)((E + 7) / 8 * 8) * 6 + 4) : 0;
   return p;
 }
 
@@ -500,9 +552,10 @@ hipError_t launch_route(const RouteLaunch& args, int dtype, void* workspace, hip
   const RoutePlan p = plan_route(a.T, a.E);
   a.tokens_per_wg = p.tokens_per_wg;
   if (p.wgs > 1) {
-    a.wg_counts = (int32_t*)workspace;
-    a.wg_psum = (float*)(a.wg_counts + (size_t)p.wgs * a.E);
-    a.wg_live = (int32_t*)(a.wg_psum + (size_t)p.wgs * a.E);
+    const size_t ld = (size_t)(a.E + 7) / 8 * 8;
+    a.wg_psum = (float*)workspace;
+    a.wg_counts = (uint16_t*)(a.wg_psum + p.wgs * ld);
+    a.wg_live = (int32_t*)(a.wg_counts + p.wgs * ld);
   }
   GMI_ROUTE(k_route, dtype, a.E, p.wgs, RT_THREADS, stream, a);
   hipError_t e = hipGetLastError();

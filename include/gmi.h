@@ -523,7 +523,7 @@ size_t gmi_moe_route_workspace_bytes(int32_t tokens, int32_t experts);
  *   tokens    >= 0, tokens * k < 2^31; experts 1 .. 1024; k 1 .. min(16, experts).
  *   logits    [tokens][ld], dtype GMI_F16, GMI_BF16 or GMI_F32, ld >= experts.
  *   mask      bytes [tokens], 0 for tokens left out; NULL keeps all.
- *   workspace gmi_moe_route_workspace_bytes(tokens, experts) bytes, 4-byte
+ *   workspace gmi_moe_route_workspace_bytes(tokens, experts) bytes, 16-byte
  *             aligned; may be NULL when that is 0. */
 gmi_status gmi_moe_route(int32_t tokens, int32_t experts, int32_t k, const void* logits, int64_t ld, gmi_dtype dtype,
                          const uint8_t* mask, int32_t renormalize, int32_t* indices, float* weights, int32_t* counts,
