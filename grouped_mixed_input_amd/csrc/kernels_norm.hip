@@ -72,8 +72,23 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 
 constexpr float kF8Max = 448.0f;
 
+// One 16-byte access, past the caches (NT) where the tensors are too large to
+// be found there by the next kernel.
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const uint16_t* p) {
+  if constexpr (NT) return __builtin_nontemporal_load((const u32x4*)p);
+  return *(const u32x4*)p;
+}
+template <bool NT, class V>
+__device__ __forceinline__ void store(void* p, V v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, (V*)p);
+  else
+    *(V*)p = v;
+}
+
 // Workgroups of WG threads, WG / TPR rows at a time.
-template <int DT, int WG, int TPR, int CPT>
+template <int DT, bool NT, int WG, int TPR, int CPT>
 __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
   __shared__ float red[WG / 64];
   const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -87,8 +102,8 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * TPR;
     const bool in = live && c < chunks;
-    xv[i] = in ? *(const u32x4*)(x + 8 * c) : u32x4{};
-    rv[i] = in && res ? *(const u32x4*)(res + 8 * c) : u32x4{};
+    xv[i] = in ? load16<NT>(x + 8 * c) : u32x4{};
+    rv[i] = in && res ? load16<NT>(res + 8 * c) : u32x4{};
   }
   float h[CPT][8];
   float ss = 0.0f;
@@ -103,7 +118,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
       ss = __builtin_fmaf(h[i][e], h[i][e], ss);
     }
     const int c = t + i * TPR;
-    if (a.h && live && c < chunks) *(u32x4*)(a.h + row * a.ldh + 8 * c) = pack8<DT>(h[i]);
+    if (a.h && live && c < chunks) store<NT>(a.h + row * a.ldh + 8 * c, pack8<DT>(h[i]));
   }
   ss = team_sum<TPR>(ss, red);
   const float r = 1.0f / sqrtf(ss / (float)a.K + a.eps);
@@ -119,7 +134,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
       h[i][e] = h[i][e] * r * w[e];
       amax = fmaxf(amax, fabsf(h[i][e]));
     }
-    if (a.y && in) *(u32x4*)(a.y + row * a.ldy + 8 * c) = pack8<DT>(h[i]);
+    if (a.y && in) store<NT>(a.y + row * a.ldy + 8 * c, pack8<DT>(h[i]));
     if (!a.q) continue;
     // 16 neighbouring threads hold one block of 128 columns (those past K
     // hold zeros); the bound keeps the scale of an all-zero block normal
@@ -131,7 +146,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
       lo = __builtin_amdgcn_cvt_pk_fp8_f32(h[i][2] * inv, h[i][3] * inv, lo, true);
       hi = __builtin_amdgcn_cvt_pk_fp8_f32(h[i][4] * inv, h[i][5] * inv, hi, false);
       hi = __builtin_amdgcn_cvt_pk_fp8_f32(h[i][6] * inv, h[i][7] * inv, hi, true);
-      *(u32x2*)(a.q + row * a.ldq + 8 * c) = u32x2{(uint32_t)lo, (uint32_t)hi};
+      store<NT>(a.q + row * a.ldq + 8 * c, u32x2{(uint32_t)lo, (uint32_t)hi});
       if (c % 16 == 0) a.scales[row * a.lds + c / 16] = s;
     }
   }
@@ -141,7 +156,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
 // weight's gradient in registers, adds the teams of a workgroup in LDS (in a
 // fixed order) and writes one fp32 row of partials per workgroup, which
 // k_norm_dweight sums in workgroup order.
-template <int DT, int WG, int TPR, int CPT>
+template <int DT, bool NT, int WG, int TPR, int CPT>
 __global__ __launch_bounds__(WG) void k_rmsnorm_bwd(NormBwdLaunch a) {
   __shared__ float red[WG / 64];
   const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -165,9 +180,9 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_bwd(NormBwdLaunch a) {
     for (int i = 0; i < CPT; ++i) {
       const int c = t + i * TPR;
       const bool in = live && c < chunks;
-      hv[i] = in ? *(const u32x4*)(a.h + row * a.ldh + 8 * c) : u32x4{};
-      gv[i] = in ? *(const u32x4*)(a.dy + row * a.lddy + 8 * c) : u32x4{};
-      rv[i] = in && a.dres ? *(const u32x4*)(a.dres + row * a.lddr + 8 * c) : u32x4{};
+      hv[i] = in ? load16<NT>(a.h + row * a.ldh + 8 * c) : u32x4{};
+      gv[i] = in ? load16<NT>(a.dy + row * a.lddy + 8 * c) : u32x4{};
+      rv[i] = in && a.dres ? load16<NT>(a.dres + row * a.lddr + 8 * c) : u32x4{};
     }
     float ss = 0.0f, gh = 0.0f;
 #pragma unroll
@@ -200,7 +215,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_bwd(NormBwdLaunch a) {
         d[e] = __builtin_fmaf(r, __builtin_fmaf(-h[e], m, g[e] * w[e]), d[e]);
         dw[i][e] = __builtin_fmaf(g[e], h[e] * r, dw[i][e]);
       }
-      if (live && c < chunks) *(u32x4*)(a.dh + row * a.lddh + 8 * c) = pack8<DT>(d);
+      if (live && c < chunks) store<NT>(a.dh + row * a.lddh + 8 * c, pack8<DT>(d));
     }
   }
   if (!a.partial) return;
@@ -234,65 +249,77 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_bwd(NormBwdLaunch a) {
   }
 }
 
-// dweight[k] = sum of the partial rows in order: 16 row lanes per column, each
-// over a contiguous range of rows, added in a fixed order.
+// dweight[k] = sum of the partial rows in order: 32 columns a workgroup, four a
+// thread, 32 threads over contiguous ranges of rows, added in a fixed order.
 __global__ __launch_bounds__(256) void k_norm_dweight(const float* partial, int parts, int K, float* dweight) {
-  __shared__ float red[16][17];
-  const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + cl;
-  const int per = (parts + 15) / 16;
-  float v = 0.0f;
+  __shared__ f32x4 red[32][8];
+  const int cl = threadIdx.x & 7, rl = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + 4 * cl;  // K is a multiple of 8
+  const int per = (parts + 31) / 32;
+  f32x4 v{};
   if (col < K) {
     const int end = min(parts, (rl + 1) * per);
 #pragma unroll 8
-    for (int p = rl * per; p < end; ++p) v += partial[(int64_t)p * K + col];
+    for (int p = rl * per; p < end; ++p) v += *(const f32x4*)(partial + (int64_t)p * K + col);
   }
   red[rl][cl] = v;
   __syncthreads();
-  if (rl == 0 && col < K) {
-    v = 0.0f;
+  if (threadIdx.x < 32 && blockIdx.x * 32 + (int)threadIdx.x < K) {
+    float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][cl];
-    dweight[col] = v;
+    for (int i = 0; i < 32; ++i) t += red[i][threadIdx.x >> 2][threadIdx.x & 3];
+    dweight[blockIdx.x * 32 + threadIdx.x] = t;
   }
 }
 
-// Threads per row and chunks per thread.  Many rows: one wave per row up to
-// 4096 columns (no barriers, eight 16-byte loads of each input in flight per
-// lane), then four and eight waves.  Few rows cannot fill the device with one
-// wave each, so the row is spread over 256 threads for latency.
+// Threads per row and chunks per thread.  Many rows: the fewest threads that
+// hold a row in four chunks each (with eight the backward needs 378 registers
+// a lane and one wave is left per SIMD: 104 us against 89 at 16384 x 4096 with
+// two waves a row).  Few rows cannot fill the device that way, so the row is
+// spread over 256 threads for latency.
+// nt: from 2^25 elements on (the tensors of a call then pass 256 MB together,
+// the size of the memory-side cache): 16384 x 4096 92 to 82 us, backward 112 to
+// 104.
 struct NormShape {
   int tpr, cpt;
+  bool nt;
 };
 static NormShape norm_shape(int64_t rows, int K) {
   const int chunks = K / 8;
   const int few = 4 * device_cu_count();
-  int tpr = chunks <= 8 * 64 ? 64 : chunks <= 8 * 256 ? 256 : 512;
+  int tpr = chunks <= 4 * 64 ? 64 : chunks <= 4 * 128 ? 128 : chunks <= 4 * 256 ? 256 : 512;
   if (rows < few && chunks > 64 && tpr < 256) tpr = 256;
   int cpt = 1;
   while (cpt * tpr < chunks) cpt *= 2;
-  return {tpr, cpt};
+  return {tpr, cpt, rows * K >= int64_t(1) << 25};
 }
 
-#define GMI_NORM_CPT(KER, DT, WG, TPR, CPT, grid, stream, args)                                      \
-  case CPT: hipLaunchKernelGGL((KER<DT, WG, TPR, CPT>), dim3(grid), dim3(WG), 0, stream, args); break
-#define GMI_NORM_TPR(KER, DT, WG, TPR, cpt, grid, stream, args)    \
-  switch (cpt) {                                                   \
-    GMI_NORM_CPT(KER, DT, WG, TPR, 1, grid, stream, args);         \
-    GMI_NORM_CPT(KER, DT, WG, TPR, 2, grid, stream, args);         \
-    GMI_NORM_CPT(KER, DT, WG, TPR, 4, grid, stream, args);         \
-    default: hipLaunchKernelGGL((KER<DT, WG, TPR, 8>), dim3(grid), dim3(WG), 0, stream, args); \
-  }
+#define GMI_NORM_LAUNCH(KER, DT, NT, WG, TPR, CPT, grid, stream, args) \
+  hipLaunchKernelGGL((KER<DT, NT, WG, TPR, CPT>), dim3(grid), dim3(WG), 0, stream, args)
+#define GMI_NORM_CPT(KER, DT, NT, WG, TPR, cpt, grid, stream, args)               \
+  do {                                                                            \
+    if ((cpt) == 1) GMI_NORM_LAUNCH(KER, DT, NT, WG, TPR, 1, grid, stream, args); \
+    else if ((cpt) == 2) GMI_NORM_LAUNCH(KER, DT, NT, WG, TPR, 2, grid, stream, args); \
+    else GMI_NORM_LAUNCH(KER, DT, NT, WG, TPR, 4, grid, stream, args);            \
+  } while (0)
+#define GMI_NORM_TPR(KER, DT, NT, s, grid, stream, args)                                              \
+  do {                                                                                                \
+    if ((s).tpr == 64) GMI_NORM_CPT(KER, DT, NT, 256, 64, (s).cpt, grid, stream, args);               \
+    else if ((s).tpr == 128) GMI_NORM_LAUNCH(KER, DT, NT, 256, 128, 4, grid, stream, args);           \
+    else if ((s).tpr == 256) GMI_NORM_CPT(KER, DT, NT, 256, 256, (s).cpt, grid, stream, args);        \
+    else if ((s).cpt <= 4) GMI_NORM_LAUNCH(KER, DT, NT, 512, 512, 4, grid, stream, args);             \
+    else GMI_NORM_LAUNCH(KER, DT, NT, 512, 512, 8, grid, stream, args);                               \
+  } while (0)
 #define GMI_NORM_DISPATCH(KER, DT, s, grid, stream, args)                    \
   do {                                                                       \
-    if ((s).tpr == 64) { GMI_NORM_TPR(KER, DT, 256, 64, (s).cpt, grid, stream, args); }         \
-    else if ((s).tpr == 256) { GMI_NORM_TPR(KER, DT, 256, 256, (s).cpt, grid, stream, args); }  \
-    else { hipLaunchKernelGGL((KER<DT, 512, 512, 8>), dim3(grid), dim3(512), 0, stream, args); } \
+    if ((s).nt) GMI_NORM_TPR(KER, DT, true, s, grid, stream, args);          \
+    else GMI_NORM_TPR(KER, DT, false, s, grid, stream, args);                \
   } while (0)
+static int norm_teams(const NormShape& s) { return s.tpr < 256 ? 256 / s.tpr : 1; }
 
 hipError_t launch_rmsnorm_quant(const NormLaunch& a, int dtype, hipStream_t stream) {
   const NormShape s = norm_shape(a.rows, a.K);
-  const int teams = s.tpr == 64 ? 4 : 1;
+  const int teams = norm_teams(s);
   const unsigned grid = (unsigned)((a.rows + teams - 1) / teams);
   if (dtype == DT_F16)
     GMI_NORM_DISPATCH(k_rmsnorm_quant, DT_F16, s, grid, stream, a);
@@ -304,7 +331,7 @@ hipError_t launch_rmsnorm_quant(const NormLaunch& a, int dtype, hipStream_t stre
 // workgroups of the backward: resident ones only, each adds one partial row
 int norm_bwd_parts(int64_t rows, int K) {
   const NormShape s = norm_shape(rows, K);
-  const int teams = s.tpr == 64 ? 4 : 1;
+  const int teams = norm_teams(s);
   const int64_t need = (rows + teams - 1) / teams, most = 2 * (int64_t)device_cu_count();
   return (int)(need < most ? need : most);
 }
@@ -313,7 +340,7 @@ hipError_t launch_rmsnorm_bwd(const NormBwdLaunch& a, int dtype, float* dweight,
   const NormShape s = norm_shape(a.rows, a.K);
   const int grid = norm_bwd_parts(a.rows, a.K);
   if (grid == 0) {  // no rows: only the zero gradient of the weight
-    hipLaunchKernelGGL(k_norm_dweight, dim3((a.K + 15) / 16), dim3(256), 0, stream, a.partial, 0, a.K, dweight);
+    hipLaunchKernelGGL(k_norm_dweight, dim3((a.K + 31) / 32), dim3(256), 0, stream, a.partial, 0, a.K, dweight);
     return hipGetLastError();
   }
   if (dtype == DT_F16)
@@ -322,7 +349,7 @@ hipError_t launch_rmsnorm_bwd(const NormBwdLaunch& a, int dtype, float* dweight,
     GMI_NORM_DISPATCH(k_rmsnorm_bwd, DT_BF16, s, grid, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dweight) return e;
-  hipLaunchKernelGGL(k_norm_dweight, dim3((a.K + 15) / 16), dim3(256), 0, stream, a.partial, grid, a.K, dweight);
+  hipLaunchKernelGGL(k_norm_dweight, dim3((a.K + 31) / 32), dim3(256), 0, stream, a.partial, grid, a.K, dweight);
   return hipGetLastError();
 }
 
