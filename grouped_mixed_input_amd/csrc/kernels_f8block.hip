@@ -47,13 +47,16 @@ __device__ __forceinline__ F8BlockLaunch k_split(F8BlockLaunch a, int split) {
   return a;
 }
 
-// Up to 16 TM rows by SK_N columns: the waves take the k-blocks in turn,
-// loading both operands from memory straight into registers (a weight is read
-// once), and add their sums through LDS in wave order.  D k-blocks per wave are
-// in flight; past the last one the loads return zeros without memory traffic.
-template <int TM, int D, int RT>
+// Up to 16 TM rows by SK_N columns: the waves take the k-blocks in turn and add
+// their sums through LDS in wave order.  Weights, read once, go from memory to
+// a ring of D slots of LDS that a wave keeps to itself (no barrier): a copy then
+// moves whole 128-byte lines of 8 rows, where loads into the instruction's
+// registers take each line in two halves.  X, in the L2 after the first
+// workgroup's reads, goes straight to registers.  Past the last k-block the
+// loads return zeros without memory traffic.
+template <int TM, int D, bool NT>
 __device__ __forceinline__ void skinny_tile(const F8BlockLaunch& a, int64_t row0, int rows, const uint8_t* W,
-                                            const float* ws, int n0, f32x4 (*red)[RT][SK_N / 16][64]) {
+                                            const float* ws, int n0, char* lds) {
   constexpr int NB = SK_N / 16;
   const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, h = lane >> 4;
   const int kb_n = (a.K + 127) / 128;
@@ -67,17 +70,30 @@ __device__ __forceinline__ void skinny_tile(const F8BlockLaunch& a, int64_t row0
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{};
-  uint32_t wo[NB], xo[TM], so[TM];
+  // copy q: rows 8 q + lane / 8 of the weights; chunk c of row n lies in slot c ^ (n / 2 % 8)
+  constexpr int WC = SK_N / 8;
+  char* const ring = lds + wave * (D * SK_N * 128);
+  uint32_t wo[WC], wc[WC], xo[TM], so[TM];
 #pragma unroll
-  for (int j = 0; j < NB; ++j)
-    wo[j] = 16 * j + r < ncols ? (uint32_t)(16 * j + r) * (uint32_t)a.ldw + h * 16 : OOB;
+  for (int q = 0; q < WC; ++q) {
+    const int n = 8 * q + (lane >> 3);
+    wc[q] = ((lane & 7) ^ ((n >> 1) & 7)) * 16;
+    wo[q] = n < ncols ? (uint32_t)n * (uint32_t)a.ldw + wc[q] : OOB;
+  }
+  uint32_t f0[NB], f1[NB];  // this lane's chunks h and h + 4 of its rows
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int n = 16 * j + r;
+    f0[j] = n * 128 + ((h ^ ((n >> 1) & 7)) << 4);
+    f1[j] = n * 128 + (((h + 4) ^ ((n >> 1) & 7)) << 4);
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const bool ok = 16 * i + r < rows;
     xo[i] = ok ? (uint32_t)(16 * i + r) * (uint32_t)a.ldx + h * 16 : OOB;
     so[i] = ok ? (uint32_t)(16 * i + r) * (uint32_t)a.ldxs * 4u : OOB;
   }
-  u32x8 w[D][NB], x[D][TM];
+  u32x8 x[D][TM];
   float sx[D][TM], sw[D];
   // column blocks start at different k-blocks: rows a power of two apart would
   // otherwise send every workgroup to the same few memory channels at a time
@@ -89,8 +105,10 @@ __device__ __forceinline__ void skinny_tile(const F8BlockLaunch& a, int64_t row0
     const uint32_t k0 = (uint32_t)kb * 128u;
     const bool in0 = (int)k0 + h * 16 < a.K, in1 = (int)k0 + h * 16 + 64 < a.K;
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-      w[d][j] = join(buf_load16s(rw, in0 ? wo[j] : OOB, k0), buf_load16s(rw, in1 ? wo[j] : OOB, k0 + 64));
+    for (int q = 0; q < WC; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(ring + d * (SK_N * 128) + q * 1024), 16,
+                                               (int)(k0 + wc[q] < (uint32_t)a.K ? wo[q] : OOB), (int)k0, 0,
+                                               NT ? CPOL_NT : 0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       x[d][i] = join(buf_load16s(rx, in0 ? xo[i] : OOB, k0), buf_load16s(rx, in1 ? xo[i] : OOB, k0 + 64));
@@ -106,21 +124,33 @@ __device__ __forceinline__ void skinny_tile(const F8BlockLaunch& a, int64_t row0
   for (int kb0 = wave; kb0 < kb_n; kb0 += D * SK_WAVES) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
+      // this slot's copies and everything behind them up to the newest D - 1
+      // k-blocks have arrived
+      wait_vm_le<(D - 1) * (WC + 3 * TM + 1)>();
+      asm volatile("" ::: "memory");
+      u32x8 w[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        w[j] = join(*(const u32x4*)(ring + d * (SK_N * 128) + f0[j]), *(const u32x4*)(ring + d * (SK_N * 128) + f1[j]));
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const float s = sx[d][i] * sw[d];  // both zero past the last k-block
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const f32x4 p = mfma16_f8(w[d][j], x[d][i], f32x4{});
+          const f32x4 p = mfma16_f8(w[j], x[d][i], f32x4{});
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(s, p[e], acc[i][j][e]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
+      wait_lgkm();  // the slot has been read
       load(d, kb0 + (d + D) * SK_WAVES);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  wait_vm_le<0>();  // the sums take the place of the rings, where nothing lands any more
+  __syncthreads();
+  f32x4(*red)[TM][NB][64] = (f32x4(*)[TM][NB][64])lds;
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -152,9 +182,12 @@ __device__ __forceinline__ void skinny_tile(const F8BlockLaunch& a, int64_t row0
 // of K.  TMAX: row blocks of 16 a workgroup holds at a time.  Up to 32 rows two
 // workgroups of 128 registers per lane share a CU; 64 rows take the registers
 // of both (capped at 128 they spill: 77 us against 66 with 128 experts).
-template <int TMAX>
+// NT: weights past the caches.
+template <int TMAX, bool NT>
 __global__ __launch_bounds__(SK_WAVES * 64, TMAX <= 2 ? 4 : 2) void k_f8_skinny(F8BlockLaunch rec) {
-  __shared__ f32x4 red[SK_WAVES][TMAX][SK_N / 16][64];
+  constexpr int D = 2;
+  static_assert(16 * TMAX * SK_N * 4 <= D * SK_N * 128, "a wave's sums fit its ring");
+  __shared__ __attribute__((aligned(16))) char lds[SK_WAVES * D * SK_N * 128];
   const F8BlockLaunch a = k_split(rec, blockIdx.z);
   const int n0 = blockIdx.x * SK_N;
   int64_t lo, hi;
@@ -173,11 +206,11 @@ __global__ __launch_bounds__(SK_WAVES * 64, TMAX <= 2 ? 4 : 2) void k_f8_skinny(
   for (int64_t m0 = lo; m0 < hi; m0 += 16 * TMAX) {
     const int rows = (int)min((int64_t)(16 * TMAX), hi - m0);
     if (rows <= 16)
-      skinny_tile<1, 1, TMAX>(a, m0, rows, W, ws, n0, red);
+      skinny_tile<1, D, NT>(a, m0, rows, W, ws, n0, lds);
     else if (rows <= 32)
-      skinny_tile<2, 1, TMAX>(a, m0, rows, W, ws, n0, red);
+      skinny_tile<2, D, NT>(a, m0, rows, W, ws, n0, lds);
     else if constexpr (TMAX > 2)
-      skinny_tile<4, 1, TMAX>(a, m0, rows, W, ws, n0, red);
+      skinny_tile<4, D, NT>(a, m0, rows, W, ws, n0, lds);
   }
 }
 
@@ -634,10 +667,14 @@ __global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, co
 
 static hipError_t launch_skinny(const F8BlockLaunch& a, hipStream_t stream) {
   const dim3 grid((a.N + SK_N - 1) / SK_N, a.offsets ? a.count : 1, a.splits);
-  if (a.offsets || a.M <= 32)
-    hipLaunchKernelGGL(k_f8_skinny<2>, grid, dim3(SK_WAVES * 64), 0, stream, a);
+  // experts whose weights pass the 256 MB of the memory-side cache together are
+  // not found there at the next call; a dense weight may be
+  if (a.offsets && (int64_t)a.count * a.N * a.K > int64_t(256) << 20)
+    hipLaunchKernelGGL((k_f8_skinny<2, true>), grid, dim3(SK_WAVES * 64), 0, stream, a);
+  else if (a.offsets || a.M <= 32)
+    hipLaunchKernelGGL((k_f8_skinny<2, false>), grid, dim3(SK_WAVES * 64), 0, stream, a);
   else
-    hipLaunchKernelGGL(k_f8_skinny<4>, grid, dim3(SK_WAVES * 64), 0, stream, a);
+    hipLaunchKernelGGL((k_f8_skinny<4, false>), grid, dim3(SK_WAVES * 64), 0, stream, a);
   return hipGetLastError();
 }
 
