@@ -1,10 +1,11 @@
 """grouped_mixed_input_amd -- grouped, mixed-input (W4A16) and implicit-conv GEMM
 for AMD MI355X (gfx950).
 
-A thin ctypes binding over the C ABI of ``libgmi.so`` (declared in
-``include/gmi.h``).  Functions here only marshal torch tensors into device
-pointers, sizes and the current HIP stream; every step of the computation runs
-in the library's HIP kernels.  There is no fallback: if ``libgmi.so`` has not
+A thin binding over the C ABI of ``libgmi.so`` (declared in
+``include/gmi.h``): ctypes, and for the calls whose device time is a few
+microseconds the native module ``_calls``.  Functions here only marshal torch
+tensors into device pointers, sizes and the current HIP stream; every step of
+the computation runs in the library's HIP kernels.  There is no fallback: if ``libgmi.so`` has not
 been built, importing the binding's functions raises.
 """
 from __future__ import annotations
@@ -417,43 +418,30 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
-def _scratch(workspace, need: int, device, stream):
-    """(address, bytes) of the caller's workspace, or of one made for this call (None without need)."""
-    if workspace is None:
-        if need == 0:
-            return None, 0
-        workspace = _new(need, torch.uint8, device, stream)
-        # the launch reads the address only, and the memory is reused in stream order
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous device tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+_native = None
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype) -> int:
-    """Checks a device matrix with unit stride along its rows; returns its leading dimension."""
-    if t.dtype is not dtype or t.shape != (rows, cols):
-        raise ValueError(f"{name} must be {dtype} [{rows}][{cols}], got {t.dtype} {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the device")
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit stride along its rows")
-    # with at most one row the stride says nothing: any legal leading dimension does
-    return ld if rows > 1 else (cols + 15) // 16 * 16
+def _bound():
+    """The native marshalling of the calls below, bound to the loaded libgmi.so.  It checks types, shapes, strides and
+    devices (ValueError) and returns the library's status."""
+    global _native
+    if _native is None:
+        L = lib()
+        try:
+            from . import _calls as native
+        except ImportError as e:
+            raise RuntimeError("the module _calls is not built; run __graft_entry__.build() or "
+                               "python -m grouped_mixed_input_amd.build") from e
+        native.bind(*(ctypes.cast(f, _p).value for f in (
+            L.gmi_rmsnorm_quant, L.gmi_rmsnorm_bwd, L.gmi_gemm_f8_block, L.gmi_gemm_f8_block_grouped, L.gmi_moe_route,
+            L.gmi_moe_route_bwd)), _stream)
+        _native = native
+    return _native
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype) -> int:
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous device tensor of {n} {dtype}")
-    return t.data_ptr()
-
-
-def _mask(mask, tokens: int):
-    if mask is None:
-        return None
-    if mask.dtype not in (torch.bool, torch.uint8):
-        raise ValueError("mask must be bool or uint8")
-    return _vector(mask, "mask", tokens, mask.dtype)
+def _scratch(need: int, device, stream):
+    """A workspace made for one call (None without need); the memory is reused in stream order."""
+    return _new((need,), torch.uint8, device, stream) if need else None
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -463,30 +451,16 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     128 columns.  x [rows][K] float16 or bfloat16.  `h` (the sum, in x's type; may be x or residual) and `y` (v in
     x's type) are written where given.  Returns (q, scales), float8_e4m3fn [rows][K] and float32
     [rows][ceil(K / 128)]; with quantize=False only `y` (made if not given) is written and returned."""
-    rows, K = x.shape
-    dt = x.dtype
-    if dt not in (torch.float16, torch.bfloat16):
-        raise ValueError("x must be float16 or bfloat16")
-    ldx = _matrix(x, "x", rows, K, dt)
     if quantize:
         if q is None:
-            q = _new((rows, K), torch.float8_e4m3fn, x.device, stream)
+            q = _new(x.shape, torch.float8_e4m3fn, x.device, stream)
         if scales is None:
-            scales = _new((rows, _scale_blocks(K)), torch.float32, x.device, stream)
-        ldq = _matrix(q, "q", rows, K, torch.float8_e4m3fn)
-        lds = _matrix(scales, "scales", rows, _scale_blocks(K), torch.float32)
-    else:
-        if q is not None or scales is not None:
-            raise ValueError("q and scales are written with quantize=True only")
-        if y is None:
-            y = _new((rows, K), dt, x.device, stream)
-        ldq = lds = 0
-    ldr = _matrix(residual, "residual", rows, K, dt) if residual is not None else 0
-    ldh = _matrix(h, "h", rows, K, dt) if h is not None else 0
-    ldy = _matrix(y, "y", rows, K, dt) if y is not None else 0
-    _check(lib().gmi_rmsnorm_quant(rows, K, x.data_ptr(), ldx, _ptr(residual), ldr, _vector(weight, "weight", K, dt),
-                                   eps, _DT[dt], _ptr(h), ldh, _ptr(y), ldy, _ptr(q), ldq, _ptr(scales), lds,
-                                   _stream(stream)))
+            scales = _new((x.shape[0], _scale_blocks(x.shape[1])), torch.float32, x.device, stream)
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales are written with quantize=True only")
+    elif y is None:
+        y = _new(x.shape, x.dtype, x.device, stream)
+    _check(_bound().rmsnorm_quant(x, weight, residual, eps, h, y, q, scales, stream))
     return (q, scales) if quantize else y
 
 
@@ -496,27 +470,17 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dres: t
     """Gradients of rmsnorm_quant's norm: `dy` is that of v, `h` the sum the forward wrote, `dres` the gradient that
     reaches h past the norm.  Returns (dh, dweight): dh in h's type (the gradient of x and of residual), dweight
     float32 [K]."""
-    rows, K = h.shape
-    dt = h.dtype
-    if dt not in (torch.float16, torch.bfloat16):
-        raise ValueError("h must be float16 or bfloat16")
     if dh is None:
-        dh = _new((rows, K), dt, h.device, stream)
+        dh = _new(h.shape, h.dtype, h.device, stream)
     if dweight is None:
-        dweight = _new((K,), torch.float32, h.device, stream)
-    ws, nbytes = _scratch(workspace, lib().gmi_rmsnorm_bwd_workspace_bytes(rows, K) if workspace is None else 0,
-                          h.device, stream)
-    _check(lib().gmi_rmsnorm_bwd(rows, K, dy.data_ptr(), _matrix(dy, "dy", rows, K, dt), h.data_ptr(),
-                                 _matrix(h, "h", rows, K, dt), _vector(weight, "weight", K, dt), _ptr(dres),
-                                 _matrix(dres, "dres", rows, K, dt) if dres is not None else 0, eps, _DT[dt],
-                                 dh.data_ptr(), _matrix(dh, "dh", rows, K, dt),
-                                 _vector(dweight, "dweight", K, torch.float32), ws, nbytes, _stream(stream)))
+        dweight = _new((h.shape[1],), torch.float32, h.device, stream)
+    if workspace is None:
+        workspace = _scratch(lib().gmi_rmsnorm_bwd_workspace_bytes(*h.shape), h.device, stream)
+    _check(_bound().rmsnorm_bwd(dy, h, weight, dres, eps, dh, dweight, workspace, stream))
     return dh, dweight
 
 
-def _f8_out(Y, rows: int, N: int, device, stream) -> torch.Tensor:
-    if Y is not None:
-        return Y
+def _f8_out(rows: int, N: int, device, stream) -> torch.Tensor:
     return _new((rows, (N + 7) // 8 * 8), torch.bfloat16, device, stream)[:, :N]
 
 
@@ -525,17 +489,12 @@ def gemm_f8_block(X: torch.Tensor, x_scales: torch.Tensor, W: torch.Tensor, w_sc
     """Y = X W^T over block-scaled fp8: X float8_e4m3fn [M][K] with x_scales float32 [M][ceil(K / 128)], W
     float8_e4m3fn [N][K] with w_scales float32 [ceil(N / 128)][ceil(K / 128)]; Y bfloat16 [M][N].  `workspace` as
     for gemm_w4a16 (an empty tensor runs unsplit)."""
-    M, K = X.shape
-    N = W.shape[0]
-    f8, kb = torch.float8_e4m3fn, _scale_blocks(K)
-    Y = _f8_out(Y, M, N, X.device, stream)
-    ws, nbytes = _scratch(workspace, lib().gmi_gemm_f8_block_workspace_bytes(M, N, K) if workspace is None else 0,
-                          X.device, stream)
-    _check(lib().gmi_gemm_f8_block(M, N, K, X.data_ptr(), _matrix(X, "X", M, K, f8), x_scales.data_ptr(),
-                                   _matrix(x_scales, "x_scales", M, kb, torch.float32), W.data_ptr(),
-                                   _matrix(W, "W", N, K, f8), w_scales.data_ptr(),
-                                   _matrix(w_scales, "w_scales", _scale_blocks(N), kb, torch.float32), Y.data_ptr(),
-                                   _matrix(Y, "Y", M, N, torch.bfloat16), ws or None, nbytes, _stream(stream)))
+    if Y is None:
+        Y = _f8_out(X.shape[0], W.shape[0], X.device, stream)
+    if workspace is None:
+        need = lib().gmi_gemm_f8_block_workspace_bytes(X.shape[0], W.shape[0], X.shape[1])
+        workspace = _scratch(need, X.device, stream)
+    _check(_bound().gemm_f8_block(X, x_scales, W, w_scales, Y, workspace, stream))
     return Y
 
 
@@ -545,22 +504,15 @@ def gemm_f8_block_grouped(offsets: torch.Tensor, X: torch.Tensor, x_scales: torc
     """gemm_f8_block per group: rows offsets[g] .. offsets[g + 1] of X and Y belong to group g with weight W[g] (W
     [groups][N][K]) and scales w_scales[g].  `offsets` is a device int32 tensor of groups + 1 entries, as moe_route
     writes it; rows outside every group are not written."""
-    rows, K = X.shape
-    if W.dim() != 3 or w_scales.dim() != 3 or w_scales.shape[0] != W.shape[0]:
-        raise ValueError("W must be [groups][N][K] and w_scales [groups][ceil(N / 128)][ceil(K / 128)]")
-    count, N, _ = W.shape
-    f8, kb = torch.float8_e4m3fn, _scale_blocks(K)
-    if count == 0:
-        return _f8_out(Y, rows, N, X.device, stream)
-    Y = _f8_out(Y, rows, N, X.device, stream)
-    ws, nbytes = _scratch(workspace, lib().gmi_gemm_f8_block_grouped_workspace_bytes(count) if workspace is None
-                          else 0, X.device, stream)
-    _check(lib().gmi_gemm_f8_block_grouped(
-        count, _vector(offsets, "offsets", count + 1, torch.int32), rows, N, K, X.data_ptr(),
-        _matrix(X, "X", rows, K, f8), x_scales.data_ptr(), _matrix(x_scales, "x_scales", rows, kb, torch.float32),
-        W.data_ptr(), _matrix(W[0], "W[0]", N, K, f8), W.stride(0), w_scales.data_ptr(),
-        _matrix(w_scales[0], "w_scales[0]", _scale_blocks(N), kb, torch.float32), w_scales.stride(0), Y.data_ptr(),
-        _matrix(Y, "Y", rows, N, torch.bfloat16), ws, nbytes, _stream(stream)))
+    if W.dim() != 3:
+        raise ValueError("W must be [groups][N][K]")
+    if Y is None:
+        Y = _f8_out(X.shape[0], W.shape[1], X.device, stream)
+    if W.shape[0] == 0:
+        return Y
+    if workspace is None:
+        workspace = _scratch(lib().gmi_gemm_f8_block_grouped_workspace_bytes(W.shape[0]), X.device, stream)
+    _check(_bound().gemm_f8_block_grouped(offsets, X, x_scales, W, w_scales, Y, workspace, stream))
     return Y
 
 
@@ -578,33 +530,18 @@ class Routing(NamedTuple):
     live: torch.Tensor
 
 
-_LOGITS = {torch.float16: GMI_F16, torch.bfloat16: GMI_BF16, torch.float32: GMI_F32}
-
-
-def _logits(t: torch.Tensor):
-    if t.dim() != 2 or t.dtype not in _LOGITS:
-        raise ValueError("logits must be [tokens][experts] in float16, bfloat16 or float32")
-    return _matrix(t, "logits", t.shape[0], t.shape[1], t.dtype)
-
-
 def moe_route(logits: torch.Tensor, k: int, mask: torch.Tensor | None = None, renormalize: bool = True,
               out: Routing | None = None, workspace: torch.Tensor | None = None, stream=None) -> Routing:
     """Top-k routing of logits [tokens][experts] with the balance loss; see Routing.  `mask` (bool or uint8
     [tokens]) leaves tokens out: their slots hold expert -1.  `out` receives the results where given."""
-    T, E = logits.shape
-    ld = _logits(logits)
     if out is None:
-        dev, i32, f32 = logits.device, torch.int32, torch.float32
+        (T, E), dev, i32, f32 = logits.shape, logits.device, torch.int32, torch.float32
         out = Routing(_new((T, k), i32, dev, stream), _new((T, k), f32, dev, stream), _new((E,), i32, dev, stream),
                       _new((E + 1,), i32, dev, stream), _new((T, k), i32, dev, stream), _new((T * k,), i32, dev, stream),
                       _new((1,), f32, dev, stream), _new((1,), i32, dev, stream))
-    sizes = (T * k, T * k, E, E + 1, T * k, T * k, 1, 1)
-    ptrs = [_vector(t, name, n, torch.float32 if name in ("weights", "loss") else torch.int32)
-            for t, name, n in zip(out, Routing._fields, sizes)]
-    ws, nbytes = _scratch(workspace, lib().gmi_moe_route_workspace_bytes(T, E) if workspace is None else 0,
-                          logits.device, stream)
-    _check(lib().gmi_moe_route(T, E, k, logits.data_ptr(), ld, _LOGITS[logits.dtype], _mask(mask, T),
-                               int(renormalize), *ptrs, ws, nbytes, _stream(stream)))
+    if workspace is None:
+        workspace = _scratch(lib().gmi_moe_route_workspace_bytes(*logits.shape), logits.device, stream)
+    _check(_bound().moe_route(logits, k, mask, renormalize, *out, workspace, stream))
     return out
 
 
@@ -613,18 +550,8 @@ def moe_route_bwd(logits: torch.Tensor, indices: torch.Tensor, weights: torch.Te
                   renormalize: bool = True, dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of moe_route's logits from `dweights` [tokens][k] (float32) and `dloss` (float32 [1], on the
     device), with what the forward call wrote; mask and renormalize as given to it."""
-    T, E = logits.shape
-    ld = _logits(logits)
-    k = indices.shape[-1]
     if dlogits is None:
-        dlogits = _new((T, E), logits.dtype, logits.device, stream)
-    ldd = _matrix(dlogits, "dlogits", T, E, logits.dtype)
-    _check(lib().gmi_moe_route_bwd(T, E, k, logits.data_ptr(), ld, _LOGITS[logits.dtype], _mask(mask, T),
-                                   int(renormalize), _vector(indices, "indices", T * k, torch.int32),
-                                   _vector(weights, "weights", T * k, torch.float32),
-                                   _vector(offsets, "offsets", E + 1, torch.int32),
-                                   _vector(live, "live", 1, torch.int32),
-                                   _vector(dweights, "dweights", T * k, torch.float32),
-                                   _vector(dloss, "dloss", 1, torch.float32), dlogits.data_ptr(), ldd,
-                                   _stream(stream)))
+        dlogits = _new(logits.shape, logits.dtype, logits.device, stream)
+    _check(_bound().moe_route_bwd(logits, indices, weights, offsets, live, dweights, dloss, mask, renormalize, dlogits,
+                                  stream))
     return dlogits

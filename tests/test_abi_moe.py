@@ -165,3 +165,27 @@ def test_binding_refuses_wrong_tensors(gmi):
         gmi.moe_route(torch.zeros(4, 8, dtype=torch.float64), 2)
     with pytest.raises(ValueError, match="device"):
         gmi.moe_route(torch.zeros(4, 8), 2)
+
+
+def test_native_marshalling_refuses_what_is_no_tensor(gmi):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x must be a tensor"):
+        gmi._bound().rmsnorm_quant([1.0], x[0], None, 1e-6, None, None, None, None, 0)
+    with pytest.raises(ValueError, match=r"\[rows\]\[K\]"):
+        gmi._bound().rmsnorm_quant(x[0], x[0], None, 1e-6, None, None, None, None, 0)
+    with pytest.raises(TypeError, match="9 arguments"):
+        gmi._bound().rmsnorm_quant(x)
+    with pytest.raises(TypeError, match="6 addresses"):
+        gmi._bound().bind(1, 2)
+    with pytest.raises(ValueError, match="NULL"):
+        gmi._bound().bind(1, 2, 3, 4, 5, 0, len)
+    with pytest.raises(ValueError, match="2\\^31|device"):
+        gmi.moe_route(x.float(), 2, out=gmi.Routing(*([x] * 8)), workspace=x)
+
+
+def test_empty_group_list_is_a_no_op(gmi):
+    f8 = torch.zeros(4, 256, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    Y = torch.full((4, 128), 3.0, dtype=torch.bfloat16)
+    got = gmi.gemm_f8_block_grouped(torch.zeros(1, dtype=torch.int32), f8, torch.ones(4, 2), f8.new_zeros(0, 128, 256),
+                                    torch.ones(0, 1, 2), Y=Y)
+    assert got is Y and (Y == 3.0).all()
