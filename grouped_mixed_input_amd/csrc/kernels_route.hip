@@ -39,6 +39,22 @@ template <int CTRL>
 __device__ __forceinline__ int dpp_i(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
+// v of this lane combined with that of the lane 16 (32) further or back, by
+// swapping rows (halves) of two copies: no trip through the LDS crossbar
+template <class T, class F>
+__device__ __forceinline__ T across16(T v, F f) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(bits, bits, false, false);
+  const uint32_t lo = r[0], hi = r[1];  // (a bit cast of a vector's element takes its first)
+  return f(__builtin_bit_cast(T, lo), __builtin_bit_cast(T, hi));
+}
+template <class T, class F>
+__device__ __forceinline__ T across32(T v, F f) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+  const uint32_t lo = r[0], hi = r[1];  // (a bit cast of a vector's element takes its first)
+  return f(__builtin_bit_cast(T, lo), __builtin_bit_cast(T, hi));
+}
 // reduction over a group of L = 16 or 64 lanes, result in every lane
 template <int L, class T, class F>
 __device__ __forceinline__ T group_reduce(T v, F f) {
@@ -47,8 +63,8 @@ __device__ __forceinline__ T group_reduce(T v, F f) {
   v = f(v, __builtin_bit_cast(T, dpp_i<0x141>(__builtin_bit_cast(int, v))));
   v = f(v, __builtin_bit_cast(T, dpp_i<0x140>(__builtin_bit_cast(int, v))));
   if constexpr (L == 64) {
-    v = f(v, __shfl_xor(v, 16));
-    v = f(v, __shfl_xor(v, 32));
+    v = across16(v, f);
+    v = across32(v, f);
   }
   return v;
 }
@@ -90,12 +106,15 @@ __device__ __forceinline__ uint32_t packed_key(float f, int e) {
 // RT_THREADS workgroup; returns this thread's, and the total in `total`.
 __device__ __forceinline__ int block_scan(int v, int* wave_sums, int& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // inside rows of 16 lanes, then the last lane of a row onto the next one and
+  // that of the lower half onto the upper
   int s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(s, d);
-    if (lane >= d) s += o;
-  }
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);
   __syncthreads();
   if (lane == 63) wave_sums[wave] = s;
   __syncthreads();
@@ -149,6 +168,9 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
 #pragma unroll
   for (int j = 0; j < V; ++j) psum[j] = 0.0f;
   int live_here = 0;
+  // a single workgroup with a group per token keeps slot and rank at hand
+  int my_sel = -1, my_rank = -1;
+  const bool direct = GROUPS == RT_PASS && gridDim.x == 1;
   const int first = blockIdx.x * a.tokens_per_wg, end = min(a.T, first + a.tokens_per_wg);
   __syncthreads();
   for (int t0 = first; t0 < end; t0 += RT_PASS) {
@@ -228,7 +250,12 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
             r = base[sel] + __popc(mask[tl >> 5][sel] & ((1u << (tl & 31)) - 1u));
             for (int q = 0; q < tl >> 5; ++q) r += __popc(mask[q][sel]);
           }
-          a.slot_row[(int64_t)t * a.k + lane] = r;
+          if (direct) {
+            my_sel = sel;
+            my_rank = r;
+          } else {
+            a.slot_row[(int64_t)t * a.k + lane] = r;
+          }
         }
       }
     }
@@ -260,24 +287,26 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
     __syncthreads();
   }
   // sums of p over the workgroup: the wave's groups, then the waves in order
+  // (those that had a token)
+  const auto add = [](float x, float y) { return x + y; };
+  const int waves = min(RT_THREADS / 64, (end - first + 64 / L - 1) / (64 / L));
+  if ((int)threadIdx.x < 64 * waves) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    float v = psum[j];
-    if constexpr (L == 16) {
-      v += __shfl_xor(v, 16);
-      v += __shfl_xor(v, 32);
+    for (int j = 0; j < V; ++j) {
+      float v = psum[j];
+      if constexpr (L == 16) v = across32(across16(v, add), add);
+      if ((threadIdx.x & 63) < L) psum_lds[threadIdx.x >> 6][j * L + lane] = v;
     }
-    if ((threadIdx.x & 63) < L) psum_lds[threadIdx.x >> 6][j * L + lane] = v;
+    const float lf = group_sum<64>((float)live_here);
+    if ((threadIdx.x & 63) == 0) wave_i[threadIdx.x >> 6] = (int)lf;
   }
-  const float lf = group_sum<64>((float)live_here);
-  if ((threadIdx.x & 63) == 0) wave_i[threadIdx.x >> 6] = (int)lf;
   __syncthreads();
   int live_wg = 0;
-  for (int i = 0; i < RT_THREADS / 64; ++i) live_wg += wave_i[i];
+  for (int i = 0; i < waves; ++i) live_wg += wave_i[i];
   const int e = threadIdx.x;
   float ps = 0.0f;
   if (e < a.E)
-    for (int i = 0; i < RT_THREADS / 64; ++i) ps += psum_lds[i][e];
+    for (int i = 0; i < waves; ++i) ps += psum_lds[i][e];
   if (gridDim.x > 1) {
     const int ld = route_ld(a.E);
     if (e < ld) {
@@ -296,18 +325,27 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
     base[e] = off;
   }
   if (e == 0) a.offsets[a.E] = total;
-  write_loss(a, ps, cnt, total, live_wg, wave_f);
   __syncthreads();  // base now holds the offsets; ranks were written by this workgroup
   const int slots = a.T * a.k;
-  for (int s = threadIdx.x; s < slots; s += RT_THREADS) {
-    const int x = a.indices[s];
-    if (x >= 0) {
-      const int r = base[x] + a.slot_row[s];
+  if (direct) {
+    if (lane < a.k && group < a.T) {
+      const int s = group * a.k + lane, r = my_sel >= 0 ? base[my_sel] + my_rank : -1;
       a.slot_row[s] = r;
-      a.row_slot[r] = s;
+      if (r >= 0) a.row_slot[r] = s;
     }
-    if (s >= total) a.row_slot[s] = -1;
+    for (int s = total + threadIdx.x; s < slots; s += RT_THREADS) a.row_slot[s] = -1;
+  } else {
+    for (int s = threadIdx.x; s < slots; s += RT_THREADS) {
+      const int x = a.indices[s];
+      if (x >= 0) {
+        const int r = base[x] + a.slot_row[s];
+        a.slot_row[s] = r;
+        a.row_slot[r] = s;
+      }
+      if (s >= total) a.row_slot[s] = -1;
+    }
   }
+  write_loss(a, ps, cnt, total, live_wg, wave_f);
 }
 
 // Second launch: every workgroup sums the count matrix for itself (totals, and
