@@ -979,8 +979,9 @@ static gmi_status route_sizes(const char* who, int32_t tokens, int32_t experts, 
   if (experts > kMaxExperts || k > kMaxTopK)
     return fail(GMI_ERR_UNSUPPORTED, "%s: %d experts (at most %d), k %d (at most %d)", who, experts, kMaxExperts, k,
                 kMaxTopK);
-  if ((int64_t)tokens * k > INT32_MAX)
-    return fail(GMI_ERR_UNSUPPORTED, "%s: tokens * k above 2^31 - 1", who);
+  // (the kernels' token numbers run up to a workgroup's share past the last one)
+  if ((int64_t)tokens * k > INT32_MAX - (1 << 17))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: tokens * k not below 2^31 - 2^17", who);
   if (!dtype_ok(dtype) && dtype != GMI_F32)
     return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
   if (tokens > 0) {

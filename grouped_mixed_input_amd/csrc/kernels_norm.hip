@@ -317,15 +317,30 @@ static NormShape norm_shape(int64_t rows, int K) {
   } while (0)
 static int norm_teams(const NormShape& s) { return s.tpr < 256 ? 256 / s.tpr : 1; }
 
-hipError_t launch_rmsnorm_quant(const NormLaunch& a, int dtype, hipStream_t stream) {
-  const NormShape s = norm_shape(a.rows, a.K);
+hipError_t launch_rmsnorm_quant(const NormLaunch& all, int dtype, hipStream_t stream) {
+  const NormShape s = norm_shape(all.rows, all.K);
   const int teams = norm_teams(s);
-  const unsigned grid = (unsigned)((a.rows + teams - 1) / teams);
-  if (dtype == DT_F16)
-    GMI_NORM_DISPATCH(k_rmsnorm_quant, DT_F16, s, grid, stream, a);
-  else
-    GMI_NORM_DISPATCH(k_rmsnorm_quant, DT_BF16, s, grid, stream, a);
-  return hipGetLastError();
+  constexpr int64_t most = int64_t(1) << 22;  // a launch's threads stay below 2^32
+  NormLaunch a = all;
+  for (int64_t row = 0; row < all.rows; row += most) {
+    a.rows = all.rows - row < most ? all.rows - row : most;
+    a.x = all.x + row * all.ldx;
+    if (all.residual) a.residual = all.residual + row * all.ldr;
+    if (all.h) a.h = all.h + row * all.ldh;
+    if (all.y) a.y = all.y + row * all.ldy;
+    if (all.q) {
+      a.q = all.q + row * all.ldq;
+      a.scales = all.scales + row * all.lds;
+    }
+    const unsigned grid = (unsigned)((a.rows + teams - 1) / teams);
+    if (dtype == DT_F16)
+      GMI_NORM_DISPATCH(k_rmsnorm_quant, DT_F16, s, grid, stream, a);
+    else
+      GMI_NORM_DISPATCH(k_rmsnorm_quant, DT_BF16, s, grid, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // workgroups of the backward: resident ones only, each adds one partial row

@@ -419,7 +419,7 @@ gmi_status gmi_conv2d_dgrad_implicit(int32_t N, int32_t H, int32_t W, int32_t C,
  *   y = RN(v)                     (if y is given; `dtype`)
  *   s = max(max |v| over the 128-column block, 448 * 2^-126) / 448
  *   q = e4m3(v / s)               (if q is given, with scales; nearest even)
- * One launch, each input read once.  A row that holds a NaN or an infinity
+ * One launch (per 2^22 rows), each input read once.  A row that holds a NaN or an infinity
  * (or whose sum of squares passes the fp32 range) follows fp32 arithmetic.
  *   rows      >= 0 (0 is a no-op); K in 1 .. 32768, a multiple of 8.
  *   x         [rows][ldx]; residual [rows][ldr] or NULL (then h = x).
@@ -520,7 +520,7 @@ size_t gmi_moe_route_workspace_bytes(int32_t tokens, int32_t experts);
  *   live           live tokens.
  * A NaN or +infinity among a live token's logits makes its weights and the
  * loss NaN.  Every result is the same on every run.
- *   tokens    >= 0, tokens * k < 2^31; experts 1 .. 1024; k 1 .. min(16, experts).
+ *   tokens    >= 0, tokens * k < 2^31 - 2^17; experts 1 .. 1024; k 1 .. min(16, experts).
  *   logits    [tokens][ld], dtype GMI_F16, GMI_BF16 or GMI_F32, ld >= experts.
  *   mask      bytes [tokens], 0 for tokens left out; NULL keeps all.
  *   workspace gmi_moe_route_workspace_bytes(tokens, experts) bytes, 16-byte

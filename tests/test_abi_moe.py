@@ -189,3 +189,10 @@ def test_empty_group_list_is_a_no_op(gmi):
     got = gmi.gemm_f8_block_grouped(torch.zeros(1, dtype=torch.int32), f8, torch.ones(4, 2), f8.new_zeros(0, 128, 256),
                                     torch.ones(0, 1, 2), Y=Y)
     assert got is Y and (Y == 3.0).all()
+
+
+def test_route_token_limit(gmi):
+    # token numbers stay 32-bit with room for a workgroup's share past the last one
+    assert _route(gmi, T=2 ** 31 - 2 ** 17, k=1) == gmi.GMI_ERR_UNSUPPORTED
+    assert _route(gmi, T=2 ** 31 - 1, k=1) == gmi.GMI_ERR_UNSUPPORTED
+    assert _route(gmi, T=2 ** 31 - 2 ** 17 - 1, k=1, ws=None) == gmi.GMI_ERR_WORKSPACE

@@ -171,3 +171,16 @@ def test_norm_bwd_eps_zero_and_no_rows(gmi):
     dw = torch.full((64,), 7.0, device=dev())
     gmi.rmsnorm_bwd(none, none, w.to(dev()), dweight=dw)
     assert (dw == 0).all()
+
+
+def test_norm_more_rows_than_one_launch(gmi):
+    rows, K = (1 << 22) + 5, 8
+    gen = torch.Generator().manual_seed(15)
+    x, res = (torch.randn(rows, K, generator=gen).to(torch.bfloat16) for _ in range(2))
+    w = torch.ones(K, dtype=torch.bfloat16)
+    h = torch.zeros(rows, K, dtype=torch.bfloat16, device=dev())
+    q, s = gmi.rmsnorm_quant(x.to(dev()), w.to(dev()), residual=res.to(dev()), eps=1e-5, h=h)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(0, rows, 9973), torch.arange((1 << 22) - 4, rows)])
+    _check_norm(x[at], w, res[at], 1e-5, h[at.to(dev())], None, q.view(torch.uint8)[at.to(dev())].view(ref.F8),
+                s[at.to(dev())])
