@@ -247,10 +247,10 @@ __global__ __launch_bounds__(SK_WAVES * 64, TMAX <= 2 ? 4 : 2) void k_f8_skinny(
 // rows.  (A load per wave and k-tile touches a line per row and asks the L1 for
 // as many lines as the operands' copies do: 271 us against 239 without them.)
 // ---------------------------------------------------------------------------
-template <int BM_, int BN_, int WM_, int WN_, int SA_, int SB_, bool EARLY_X_, bool NT_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int SA_, int SB_, bool EARLY_X_, bool NT_ = false, int ROWS_ = BM_ / WM_>
 struct F8Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN, THREADS = 64 * NW;
-  static constexpr int WTM = BM / WM, WTN = BN / WN, MI = WTM / 16, NJ = WTN / 16;
+  static constexpr int WTM = BM / WM, WTN = BN / WN, MI = ROWS_ / 16, NJ = WTN / 16;  // (the first ROWS_ of a wave's rows)
   static constexpr int SA = SA_, SB = SB_;
   static constexpr bool EARLY_X = EARLY_X_, NT = NT_;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
@@ -566,6 +566,7 @@ using F8T128 = F8Tile<128, 128, 2, 2, 2, 2, true>;
 // of 64 rows 205 to 194 us)
 using F8S128 = F8Tile<128, 256, 2, 4, 3, 3, false, true>;
 using F8S64 = F8Tile<64, 256, 1, 8, 3, 3, false, true>;
+using F8S32 = F8Tile<64, 256, 1, 8, 3, 3, false, true, 32>;  // as F8S64, of which only 32 rows are multiplied
 constexpr int SK_ROWS = 64;        // dense rows up to which the skinny kernel runs
 constexpr int SPLIT_MOST = 8;
 constexpr int SK_ONLY_ROWS = 256;  // row capacity up to which the grouped call runs it
@@ -583,9 +584,15 @@ struct F8Lists {
   int32_t total[2];  // tiles of the long and of the short groups
   int32_t start[2][kMaxOffsetGroupCount];  // exclusive sums over the groups
 };
+// rows lo .. m (of the next group) clipped to the operand: first row and count
+__device__ __forceinline__ void clip_rows(const F8BlockLaunch& a, int& lo, int& m) {
+  lo = min(max(lo, 0), a.M);
+  m = max(min(max(m, 0), a.M) - lo, 0);
+}
 __device__ __forceinline__ void group_rows(const F8BlockLaunch& a, int g, int& lo, int& m) {
-  lo = min(max(a.offsets[g], 0), a.M);
-  m = max(min(max(a.offsets[g + 1], 0), a.M) - lo, 0);
+  lo = a.offsets[g];
+  m = a.offsets[g + 1];
+  clip_rows(a, lo, m);
 }
 
 __global__ __launch_bounds__(kMaxOffsetGroupCount) void k_f8_group_table(F8BlockLaunch a, int tn, F8Lists* lists) {
@@ -614,41 +621,71 @@ __global__ __launch_bounds__(kMaxOffsetGroupCount) void k_f8_group_table(F8Block
   }
 }
 
-// Position of a workgroup in the order of tiles: chunks of 8 neighbours, which
-// share a weight panel or rows, go to one XCD, the chunks to the XCDs in turn
-// (no chunks: 283 us against 275, and 256 against 210 with 128 rows each).
-__device__ __forceinline__ int xcd_chunk(int b) {
-  const int i = b / XCDS;
-  return ((i / 8) * XCDS + b % XCDS) * 8 + i % 8;
-}
+// Tiles go to the XCDs in chunks of CHUNK neighbours of one list, the chunks in
+// turn: a chunk of long tiles is a block of 4 by 2, a chunk of short ones mostly
+// a group's rows with all its weights, so an XCD fetches few panels for it.
+constexpr int CHUNK = 8, BAND = 4;
 
 __global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, const F8Lists* lists, int tail) {
   __shared__ __attribute__((aligned(16))) char lds[F8S128::LDS];
   static_assert(F8T256::LDS <= F8S128::LDS && F8S64::LDS <= F8S128::LDS, "one LDS block");
   static_assert(F8T256::THREADS == 512 && F8S128::THREADS == 512 && F8S64::THREADS == 512, "one workgroup size");
-  const int p = xcd_chunk(blockIdx.x), nl = lists->total[0], ns = lists->total[1];
-  if (p >= nl + ns) return;
-  // short tiles before position p: spread evenly over the long ones up to the
-  // last `tail` short tiles
-  const int spread = max(ns - tail, 0), mixed = nl + spread;
-  int cls = 1, tile = p - nl;
+  const int lane = threadIdx.x & 63, turn_of_xcd = blockIdx.x / XCDS;
+  const int p = turn_of_xcd / CHUNK * XCDS + blockIdx.x % XCDS;  // chunk
+  // All that finding the tile needs of the first 128 groups is asked for at
+  // once: one trip to memory before the first copy instead of four.
+  const int nl = lists->total[0], ns = lists->total[1];
+  int first[2][2], row[2], next[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int q = min(lane + 64 * i, a.count - 1);
+    first[i][0] = lists->start[0][q];
+    first[i][1] = lists->start[1][q];
+    row[i] = a.offsets[q];
+    next[i] = a.offsets[q + 1];
+  }
+  const int cl = (nl + CHUNK - 1) / CHUNK, cs = (ns + CHUNK - 1) / CHUNK;
+  if (p >= cl + cs) return;
+  // chunks of short tiles before chunk p: spread evenly over the long ones up
+  // to the last `tail`
+  const int spread = max(cs - tail, 0), mixed = cl + spread;
+  int cls = 1, tile = p - cl;
   if (p < mixed) {
-    const int before = (int)((int64_t)p * spread / mixed), next = (int)((int64_t)(p + 1) * spread / mixed);
-    cls = next > before;
+    const int before = (int)((int64_t)p * spread / mixed), after = (int)((int64_t)(p + 1) * spread / mixed);
+    cls = after > before;
     tile = cls ? before : p - before;
   }
+  tile = tile * CHUNK + turn_of_xcd % CHUNK;
+  if (tile >= (cls ? ns : nl)) return;
   // the last group whose first tile is not past this one
   int n = 0;
-  const int lane = threadIdx.x & 63;
-  for (int q = lane; q < a.count; q += 64) n += lists->start[cls][q] <= tile;
-  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-  const int g = __builtin_amdgcn_readfirstlane(n) - 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    n += __popcll(__ballot(lane + 64 * i < a.count && (cls ? first[i][1] : first[i][0]) <= tile));
+  if (a.count > 128) {
+    int more = 0;
+    for (int q = lane + 128; q < a.count; q += 64) more += lists->start[cls][q] <= tile;
+    for (int d = 1; d < 64; d <<= 1) more += __shfl_xor(more, d);
+    n += __builtin_amdgcn_readfirstlane(more);
+  }
+  const int g = n - 1;
   if (g < 0) return;
-  int lo, m;
-  group_rows(a, g, lo, m);
-  const int local = tile - lists->start[cls][g], tm = (m + 255) / 256, tn = (a.N + 255) / 256;
+  int lo, m, base;
+  if (g < 128) {
+    const int l = g & 63, i = g >> 6;
+    base = __builtin_amdgcn_readlane(i ? (cls ? first[1][1] : first[1][0]) : (cls ? first[0][1] : first[0][0]), l);
+    lo = __builtin_amdgcn_readlane(i ? row[1] : row[0], l);
+    m = __builtin_amdgcn_readlane(i ? next[1] : next[0], l);
+    clip_rows(a, lo, m);
+  } else {
+    group_rows(a, g, lo, m);
+    base = lists->start[cls][g];
+  }
+  const int local = tile - base, tm = (m + 255) / 256, tn = (a.N + 255) / 256;
   if ((uint32_t)local >= (uint32_t)(tm * tn)) return;  // overlapping groups: the sums may not fit
-  const int mi = local % tm, n0 = local / tm * 256, rows = m - mi * 256;
+  int mi, ni;
+  raster(local, tm, tn, mi, ni, BAND);
+  const int n0 = ni * 256, rows = m - mi * 256;
   const int64_t row0 = (int64_t)lo + (int64_t)mi * 256;
   const uint8_t* W = a.W + (int64_t)g * a.w_stride;
   const float* ws = a.ws + (int64_t)g * a.ws_stride;
@@ -661,8 +698,10 @@ __global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, co
     f8_tile<F8T256>(lds, a, row0, rows, W, ws, n0, turn);
   else if (rows > 64)
     f8_tile<F8S128>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
-  else
+  else if (rows > 32)
     f8_tile<F8S64>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
+  else
+    f8_tile<F8S32>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
 }
 
 static hipError_t launch_skinny(const F8BlockLaunch& a, hipStream_t stream) {
@@ -754,8 +793,9 @@ const int tn = (a.N + 255) / 256;
   // the tile count is known on the device only: every group with its own
   // partial tile bounds it
   const int64_t most = ((int64_t)a.M / 256 + std::min(a.count, a.M)) * tn;
-  const unsigned grid = (unsigned)((most + 8 * XCDS - 1) / (8 * XCDS) * (8 * XCDS));
-  hipLaunchKernelGGL(k_f8_tiled_grouped, dim3(grid), dim3(512), 0, stream, a, lists, device_cu_count() / 2);
+  const int64_t chunks = most / CHUNK + 2;  // each list's last one may be short
+  const unsigned grid = (unsigned)((chunks + XCDS - 1) / XCDS * XCDS * CHUNK);
+  hipLaunchKernelGGL(k_f8_tiled_grouped, dim3(grid), dim3(512), 0, stream, a, lists, device_cu_count() / (2 * CHUNK));
   return hipGetLastError();
 }
 
