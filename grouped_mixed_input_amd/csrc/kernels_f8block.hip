@@ -560,21 +560,33 @@ __global__ __launch_bounds__(256) void k_f8_join(F8BlockLaunch a) {
 
 using F8T256 = F8Tile<256, 256, 4, 2, 2, 2, true>;
 using F8T128 = F8Tile<128, 128, 2, 2, 2, 2, true>;
-// shapes of the grouped call's short tiles: the weight columns of a 256 x 256
-// tile over 128 and 64 rows, three k-tiles deep (two: 309 us against 285 in the
-// mix below); their weights are read once and pass the L2 by (nt: 128 experts
-// of 64 rows 205 to 194 us)
-using F8S128 = F8Tile<128, 256, 2, 4, 3, 3, false, true>;
-using F8S64 = F8Tile<64, 256, 1, 8, 3, 3, false, true>;
-using F8S32 = F8Tile<64, 256, 1, 8, 3, 3, false, true, 32>;  // as F8S64, of which only 32 rows are multiplied
-constexpr int SK_ROWS = 64;        // dense rows up to which the skinny kernel runs
+// The grouped call's tile shapes.  UNIT rows and columns at most, a group's last
+// rows in the smallest shape that holds them; weights of short tiles are read
+// once and pass the L2 by (nt: 128 experts of 64 rows 205 to 194 us), three
+// k-tiles deep (two: 309 us against 285 in the mix below).  TINY multiplies only
+// 32 rows.  LONG: groups of more rows than this mostly wait for the matrix pipe.
+struct F8Large {
+  static constexpr int UNIT = 256, LONG = 128, THREADS = 512, WGS = 1;
+  using Full = F8T256;
+  using Half = F8Tile<128, 256, 2, 4, 3, 3, false, true>;
+  using Short = F8Tile<64, 256, 1, 8, 3, 3, false, true>;
+  using Tiny = F8Tile<64, 256, 1, 8, 3, 3, false, true, 32>;
+};
+// where those tiles would not fill the device (4 groups, 1000 rows, N 512, K
+// 1024: 22.9 us; these take 14.5)
+struct F8Small {
+  static constexpr int UNIT = 128, LONG = 64, THREADS = 256, WGS = 2;
+  using Full = F8T128;
+  using Half = F8T128;
+  using Short = F8Tile<64, 128, 1, 4, 3, 3, false, true>;
+  using Tiny = F8Tile<64, 128, 1, 4, 3, 3, false, true, 32>;
+};
+constexpr int SK_ROWS = 64;  // rows up to which the skinny kernel runs
 constexpr int SPLIT_MOST = 8;
-constexpr int SK_ONLY_ROWS = 256;  // row capacity up to which the grouped call runs it
 
-// Tiles of the grouped call.  A group's rows are cut into tiles of 256; the
-// last one may be short and then runs in the smallest of the three shapes that
-// holds it.  Groups of more than 128 rows mostly wait for the matrix pipe, the
-// others for their weights to come from memory, so the two lists of tiles are
+// Tiles of the grouped call.  A group's rows are cut into units; long groups
+// mostly wait for the matrix pipe, short ones for their weights to come from
+// memory, so the two lists of tiles are
 // dealt out in turn, in proportion, and the device computes and reads at the
 // same time (275 us against 283 one list after the other: 128 experts, 16384
 // skewed rows, N 2048, K 4096); some short tiles are kept for the end, where
@@ -595,13 +607,13 @@ __device__ __forceinline__ void group_rows(const F8BlockLaunch& a, int g, int& l
   clip_rows(a, lo, m);
 }
 
-__global__ __launch_bounds__(kMaxOffsetGroupCount) void k_f8_group_table(F8BlockLaunch a, int tn, F8Lists* lists) {
+__global__ __launch_bounds__(kMaxOffsetGroupCount) void k_f8_group_table(F8BlockLaunch a, int unit, int above, F8Lists* lists) {
   __shared__ int32_t sums[2][kMaxOffsetGroupCount / 64];
   const int g = threadIdx.x, lane = g & 63, wave = g >> 6;
   int lo, m = 0;
   if (g < a.count) group_rows(a, g, lo, m);
-  const int tiles = (m + 255) / 256 * tn;
-  int v[2] = {m > 128 ? tiles : 0, m > 128 ? 0 : tiles}, s[2];
+  const int tiles = (m + unit - 1) / unit * ((a.N + unit - 1) / unit);
+  int v[2] = {m > above ? tiles : 0, m > above ? 0 : tiles}, s[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     s[c] = v[c];
@@ -626,10 +638,13 @@ __global__ __launch_bounds__(kMaxOffsetGroupCount) void k_f8_group_table(F8Block
 // a group's rows with all its weights, so an XCD fetches few panels for it.
 constexpr int CHUNK = 8, BAND = 4;
 
-__global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, const F8Lists* lists, int tail) {
-  __shared__ __attribute__((aligned(16))) char lds[F8S128::LDS];
-  static_assert(F8T256::LDS <= F8S128::LDS && F8S64::LDS <= F8S128::LDS, "one LDS block");
-  static_assert(F8T256::THREADS == 512 && F8S128::THREADS == 512 && F8S64::THREADS == 512, "one workgroup size");
+template <class G>
+__global__ __launch_bounds__(G::THREADS, G::WGS) void k_f8_tiled_grouped(F8BlockLaunch a, const F8Lists* lists, int tail) {
+  constexpr int FULL = G::Full::LDS, HALF = G::Half::LDS, SHORT = G::Short::LDS;
+  __shared__ __attribute__((aligned(16))) char lds[FULL > HALF ? (FULL > SHORT ? FULL : SHORT) : (HALF > SHORT ? HALF : SHORT)];
+  static_assert(G::Full::THREADS == G::THREADS && G::Half::THREADS == G::THREADS && G::Short::THREADS == G::THREADS &&
+                    G::Tiny::THREADS == G::THREADS && G::Tiny::LDS == SHORT,
+                "one workgroup size");
   const int lane = threadIdx.x & 63, turn_of_xcd = blockIdx.x / XCDS;
   const int p = turn_of_xcd / CHUNK * XCDS + blockIdx.x % XCDS;  // chunk
   // All that finding the tile needs of the first 128 groups is asked for at
@@ -681,12 +696,12 @@ __global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, co
     group_rows(a, g, lo, m);
     base = lists->start[cls][g];
   }
-  const int local = tile - base, tm = (m + 255) / 256, tn = (a.N + 255) / 256;
+  const int local = tile - base, tm = (m + G::UNIT - 1) / G::UNIT, tn = (a.N + G::UNIT - 1) / G::UNIT;
   if ((uint32_t)local >= (uint32_t)(tm * tn)) return;  // overlapping groups: the sums may not fit
   int mi, ni;
   raster(local, tm, tn, mi, ni, BAND);
-  const int n0 = ni * 256, rows = m - mi * 256;
-  const int64_t row0 = (int64_t)lo + (int64_t)mi * 256;
+  const int n0 = ni * G::UNIT, rows = m - mi * G::UNIT;
+  const int64_t row0 = (int64_t)lo + (int64_t)mi * G::UNIT;
   const uint8_t* W = a.W + (int64_t)g * a.w_stride;
   const float* ws = a.ws + (int64_t)g * a.ws_stride;
   // Where a tile starts in K: rows a power of two apart keep all workgroups on
@@ -695,13 +710,13 @@ __global__ __launch_bounds__(512, 1) void k_f8_tiled_grouped(F8BlockLaunch a, co
   // keep step, and the large ones that share rows.
   const int turn = 5 * g;
   if (rows > 128)
-    f8_tile<F8T256>(lds, a, row0, rows, W, ws, n0, turn);
+    f8_tile<typename G::Full>(lds, a, row0, rows, W, ws, n0, turn);
   else if (rows > 64)
-    f8_tile<F8S128>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
+    f8_tile<typename G::Half>(lds, a, row0, rows, W, ws, n0, turn + ni);
   else if (rows > 32)
-    f8_tile<F8S64>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
+    f8_tile<typename G::Short>(lds, a, row0, rows, W, ws, n0, turn + ni);
   else
-    f8_tile<F8S32>(lds, a, row0, rows, W, ws, n0, turn + n0 / 256);
+    f8_tile<typename G::Tiny>(lds, a, row0, rows, W, ws, n0, turn + ni);
 }
 
 static hipError_t launch_skinny(const F8BlockLaunch& a, hipStream_t stream) {
@@ -783,20 +798,31 @@ hipError_t launch_f8_block(const F8BlockLaunch& rec, void* workspace, size_t wor
   return hipGetLastError();
 }
 
-hipError_t launch_f8_block_grouped(const F8BlockLaunch& a, void* workspace, hipStream_t stream) {
-  if (a.M <= SK_ONLY_ROWS) return launch_skinny(a, stream);
-  F8Lists* lists = (F8Lists*)workspace;
-const int tn = (a.N + 255) / 256;
-  hipLaunchKernelGGL(k_f8_group_table, dim3(1), dim3(kMaxOffsetGroupCount), 0, stream, a, tn, lists);
+// tiles of a grouped call at most (how many there are is known on the device
+// only: every group may end in a partial unit)
+static int64_t most_tiles(const F8BlockLaunch& a, int unit) {
+  return ((int64_t)a.M / unit + std::min(a.count, a.M)) * (((int64_t)a.N + unit - 1) / unit);
+}
+
+template <class G>
+static hipError_t launch_tiled_grouped(const F8BlockLaunch& a, F8Lists* lists, hipStream_t stream) {
+  hipLaunchKernelGGL(k_f8_group_table, dim3(1), dim3(kMaxOffsetGroupCount), 0, stream, a, G::UNIT, G::LONG, lists);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // the tile count is known on the device only: every group with its own
-  // partial tile bounds it
-  const int64_t most = ((int64_t)a.M / 256 + std::min(a.count, a.M)) * tn;
-  const int64_t chunks = most / CHUNK + 2;  // each list's last one may be short
+  const int64_t chunks = most_tiles(a, G::UNIT) / CHUNK + 2;  // each list's last one may be short
   const unsigned grid = (unsigned)((chunks + XCDS - 1) / XCDS * XCDS * CHUNK);
-  hipLaunchKernelGGL(k_f8_tiled_grouped, dim3(grid), dim3(512), 0, stream, a, lists, device_cu_count() / (2 * CHUNK));
+  hipLaunchKernelGGL(k_f8_tiled_grouped<G>, dim3(grid), dim3(G::THREADS), 0, stream, a, lists,
+                     device_cu_count() / (2 * CHUNK));
   return hipGetLastError();
+}
+
+hipError_t launch_f8_block_grouped(const F8BlockLaunch& a, void* workspace, hipStream_t stream) {
+  // few rows in all, or two a group on average: weights alone (128 experts, 128
+  // rows 59 us; with 16 experts and 256 rows the tiles take 31.6 against 40.9)
+  if (a.M <= SK_ROWS || (a.M <= 2 * a.count && a.M <= 256)) return launch_skinny(a, stream);
+  if (most_tiles(a, F8Large::UNIT) < device_cu_count())
+    return launch_tiled_grouped<F8Small>(a, (F8Lists*)workspace, stream);
+  return launch_tiled_grouped<F8Large>(a, (F8Lists*)workspace, stream);
 }
 
 }  // namespace gmi

@@ -223,3 +223,17 @@ def test_row_scales_that_are_zero_or_not_finite_stay_in_their_rows(gmi):
         keep = torch.tensor([i for i in range(8) if i not in (2, 3)])
         _assert_close(Y[keep], X[keep], xs[keep], W, ws, "the other rows", _lost_products)
         assert torch.isfinite(Y[6:]).all()
+
+
+@pytest.mark.parametrize("K", [16, 128, 400, 640, 1152])
+def test_grouped_enough_tiles_for_the_large_shapes(gmi, K):
+    # the same row classes over more columns: 256 x 256 units on a device of 256 CUs
+    _grouped(gmi, [130, 1, 64, 65, 128, 129, 0, 256, 257, 321, 385, 513, 20], 4100, K, K + 1, first=1,
+             lost=_lost_products)
+
+
+def test_grouped_large_shapes_with_more_than_128_groups(gmi):
+    # group numbers past the two that a lane looks up at once; long groups among them
+    counts = [(5 * g) % 9 for g in range(300)]
+    counts[3], counts[140], counts[299] = 300, 200, 150
+    _grouped(gmi, counts, 300, 256, 9, lost=_lost_products)
