@@ -296,7 +296,8 @@ struct F8Loader {
   }
   __device__ __forceinline__ void issue(int i, int kt, char* tile) const {
     const uint32_t o = kt * 128 + kc < K ? voff[i] : OOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(tile + (NW * i + wave_id()) * 1024), 16, (int)o, (int)(kt * 128), 0, NTW ? 2 : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(tile + (NW * i + wave_id()) * 1024), 16, (int)o,
+                                             (int)(kt * 128), 0, NTW ? CPOL_NT : 0);
   }
 };
 
@@ -323,7 +324,8 @@ __device__ __forceinline__ void f8_tile(char* lds, const F8BlockLaunch& a, int64
   F8Loader<T::PB, T::NW, true, T::NT> bl;
   al.init(a.X, a.ldx, row0, rows, a.K);
   bl.init(W, a.ldw, n0, cols, a.K);
-  const rsrc_t rxs = make_rsrc(a.xs + row0 * a.ldxs, (uint32_t)((int64_t)(rows < T::BM ? rows - 1 : T::BM - 1) * a.ldxs + nk) * 4u);
+  const rsrc_t rxs = make_rsrc(
+      a.xs + row0 * a.ldxs, (uint32_t)((int64_t)(rows < T::BM ? rows - 1 : T::BM - 1) * a.ldxs + nk) * 4u);
   // the wave's columns lie in one block of 128 weight rows (past N any will
   // do: those results are dropped)
   uniform_float* wsr = (uniform_float*)(uint64_t)(ws + (n0 + wn < a.N ? (int64_t)((n0 + wn) / 128) * a.ldws : 0));
