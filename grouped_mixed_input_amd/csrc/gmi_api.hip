@@ -890,15 +890,18 @@ static gmi_status f8_block_prepare(const char* who, int32_t M, int32_t N, int32_
   a.M = M;
   a.N = N;
   a.K = K;
-  a.X = (const uint8_t*)X;
-  a.W = (const uint8_t*)W;
-  a.xs = xs;
-  a.ws = ws;
+  // without k no operand is read: their leading dimensions, which nothing
+  // checks then, must not size the resources that the kernels' loads go through
+  const bool read = K > 0;
+  a.X = read ? (const uint8_t*)X : nullptr;
+  a.W = read ? (const uint8_t*)W : nullptr;
+  a.xs = read ? xs : nullptr;
+  a.ws = read ? ws : nullptr;
   a.Y = (uint16_t*)Y;
-  a.ldx = ldx;
-  a.ldxs = ldxs;
-  a.ldw = ldw;
-  a.ldws = ldws;
+  a.ldx = read ? ldx : 0;
+  a.ldxs = read ? ldxs : 0;
+  a.ldw = read ? ldw : 0;
+  a.ldws = read ? ldws : 0;
   a.ldy = ldy;
   a.offsets = nullptr;
   a.count = 0;
@@ -965,8 +968,8 @@ gmi_status gmi_gemm_f8_block_grouped(int32_t count, const int32_t* offsets, int3
   if (!aligned16(workspace)) return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
   a.offsets = offsets;
   a.count = count;
-  a.w_stride = w_stride;
-  a.ws_stride = ws_stride;
+  a.w_stride = K > 0 ? w_stride : 0;
+  a.ws_stride = K > 0 ? ws_stride : 0;
   return hip_status(launch_f8_block_grouped(a, workspace, (hipStream_t)stream), who);
 }
 

@@ -475,7 +475,8 @@ size_t gmi_gemm_f8_block_workspace_bytes(int32_t M, int32_t N, int32_t K);
  *             K (fp32 partials, summed in order by a second launch); NULL or
  *             smaller runs unsplit.
  * K, ldx and ldw multiples of 16, else GMI_ERR_UNSUPPORTED; N and M are free.
- * M == 0 or N == 0 is a no-op; K == 0 gives zeros. */
+ * M == 0 or N == 0 is a no-op; K == 0 gives zeros (X, W and their scales are
+ * not read then and may be NULL, their leading dimensions anything). */
 gmi_status gmi_gemm_f8_block(int32_t M, int32_t N, int32_t K, const void* X, int64_t ldx, const float* x_scales,
                              int64_t ldxs, const void* W, int64_t ldw, const float* w_scales, int64_t ldws, void* Y,
                              int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
