@@ -408,13 +408,17 @@ def _scale_blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor this call makes.  It belongs to the current stream; if the work runs on another one, the allocator
-    is told, so that its memory is not handed out again before that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-        t.record_stream(s)
+def _new(shape, dtype, device, stream, returned=True) -> torch.Tensor:
+    """A tensor this call makes, from the memory of the stream that the call runs on: memory let go on another stream
+    may still be in use there.  A tensor that is returned is used and let go by the caller's current stream as well,
+    so the allocator hears of that one too."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -441,7 +445,7 @@ def _bound():
 
 def _scratch(need: int, device, stream):
     """A workspace made for one call (None without need); the memory is reused in stream order."""
-    return _new((need,), torch.uint8, device, stream) if need else None
+    return _new((need,), torch.uint8, device, stream, returned=False) if need else None
 
 
 def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
