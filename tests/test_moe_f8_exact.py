@@ -227,3 +227,28 @@ def test_whole_numbers_dense(gmi, M, N, K):
                                         ([1, 0, 3, 0, 2, 1, 0, 9], 384, 1040)])
 def test_whole_numbers_grouped(gmi, counts, N, K):
     grouped(gmi, counts, N, K, 80 + K, draw_whole, check_equal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [4, 40, 100, 300])
+def test_small_products_beside_a_large_one(gmi, M):
+    # Every eight: one product of 65536, of one sign in the first block and of the other in the second, and seven of 7.5
+    # with one sign, just below its truncation step of 8.  The large ones cancel; of the small ones' 1680 the
+    # instruction keeps nothing, within its bound of 7 * 2^-13 of each eight's largest.  Row 0 without large products
+    # keeps all.
+    N, K = 72, 256
+    x = torch.full((M, K), 2.5)
+    x[:, ::8] = 256.0
+    x[:, 128::8] = -256.0
+    x[0, ::8] = 0.0
+    w = torch.full((N, K), 3.0)
+    w[:, ::8] = 256.0
+    X, W = x.to(ref.F8), w.to(ref.F8)
+    xs, ws = torch.ones(M, 2), torch.ones(1, 2)
+    off = torch.tensor([0, M], dtype=torch.int32, device=dev())
+    args = [t.to(dev()) for t in (X, xs, W, ws)]
+    for Y in (gmi.gemm_f8_block(*args), gmi.gemm_f8_block_grouped(off, *args[:2], args[2][None], args[3][None])):
+        y, (r, mag) = Y.cpu().double(), ref.gemm(X, xs, W, ws)
+        assert outside(Y, X, xs, W, ws) == 0
+        assert (r == 1680).all() and (y[0] == 1680).all() and (y[1:] == 0).all()
+        assert ((y - r).abs() <= 7 * 2.0 ** -13 * mag).all()
