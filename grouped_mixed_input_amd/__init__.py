@@ -470,16 +470,19 @@ def rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
 
 def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, dres: torch.Tensor | None = None,
                 eps: float = 1e-6, dh: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
-                workspace: torch.Tensor | None = None, stream=None):
+                workspace: torch.Tensor | None = None, stream=None, weight_grad: bool = True):
     """Gradients of rmsnorm_quant's norm: `dy` is that of v, `h` the sum the forward wrote, `dres` the gradient that
     reaches h past the norm.  Returns (dh, dweight): dh in h's type (the gradient of x and of residual), dweight
-    float32 [K]."""
+    float32 [K].  With weight_grad=False (a frozen norm) dweight is None: one launch, and no workspace."""
     if dh is None:
         dh = _new(h.shape, h.dtype, h.device, stream)
-    if dweight is None:
-        dweight = _new((h.shape[1],), torch.float32, h.device, stream)
-    if workspace is None:
-        workspace = _scratch(lib().gmi_rmsnorm_bwd_workspace_bytes(*h.shape), h.device, stream)
+    if weight_grad:
+        if dweight is None:
+            dweight = _new((h.shape[1],), torch.float32, h.device, stream)
+        if workspace is None:
+            workspace = _scratch(lib().gmi_rmsnorm_bwd_workspace_bytes(*h.shape), h.device, stream)
+    elif dweight is not None:
+        raise ValueError("dweight is written with weight_grad=True only")
     _check(_bound().rmsnorm_bwd(dy, h, weight, dres, eps, dh, dweight, workspace, stream))
     return dh, dweight
 

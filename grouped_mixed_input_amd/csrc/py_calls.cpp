@@ -191,7 +191,7 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Matrix dy = matrix(a[0], "dy", rows, K, type), mh = matrix(a[1], "h", rows, K, type),
                  dres = matrix_or_none(a[3], "dres", rows, K, type), dh = matrix(a[5], "dh", rows, K, type);
     const void* w = vector(a[2], "weight", K, type);
-    float* dw = (float*)vector(a[6], "dweight", K, F32);
+    float* dw = a[6] == Py_None ? nullptr : (float*)vector(a[6], "dweight", K, F32);
     const Scratch ws = scratch(a[7]);
     const float eps = real(a[4]);
     const int32_t r32 = size32(rows, "rows"), k32 = size32(K, "K");
