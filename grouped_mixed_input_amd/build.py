@@ -69,11 +69,12 @@ def build(jobs: int | None = None) -> pathlib.Path:
     with cf.ThreadPoolExecutor(jobs) as ex:
         calls = ex.submit(_build_calls)
         list(ex.map(lambda so: _compile(CSRC / so[0], so[1]), zip(SOURCES, objs)))
+        tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
+        cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
+        subprocess.run(cmd, check=True, capture_output=True, text=True)
+        os.replace(tmp, LIB)
+        # libgmi.so needs hipcc alone and stands by now, whatever becomes of the module for Python
         calls.result()
-    tmp = LIB.with_suffix(".so.tmp%d" % os.getpid())
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *map(str, objs), "-o", str(tmp)]
-    subprocess.run(cmd, check=True, capture_output=True, text=True)
-    os.replace(tmp, LIB)
     return LIB
 
 
