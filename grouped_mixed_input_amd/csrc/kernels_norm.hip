@@ -13,8 +13,8 @@
 // are fp32; h, y and dh are rounded once to the 16-bit type.  y is formed
 // from the unrounded fp32 sum x + residual.
 //
-// Bound by memory: 16384 x 4096 bf16 78 us forward (6.1 TB/s), 88 + 4.6 backward
-// (6.1 TB/s in the main launch; a plain copy reaches 5.4).  One row of 4096:
+// Bound by memory: 16384 x 4096 bf16 73 us forward (6.5 TB/s), 90 + 4.6 backward
+// (6.0 TB/s in the main launch; a plain copy reaches 5.4).  One row of 4096:
 // 2.5 us, an empty launch's time.
 #include "gmi_device.hpp"
 #include "gmi_internal.hpp"
@@ -76,8 +76,7 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 
 constexpr float kF8Max = 448.0f;
 
-// One 16-byte access, past the caches (NT) where the tensors are too large to
-// be found there by the next kernel.
+// One 16-byte access, or past the caches (NT).
 template <bool NT>
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) {
   if constexpr (NT) return __builtin_nontemporal_load((const u32x4*)p);
@@ -138,7 +137,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
       h[i][e] = h[i][e] * r * w[e];
       amax = fmaxf(amax, fabsf(h[i][e]));
     }
-    if (a.y && in) store<NT>(a.y + row * a.ldy + 8 * c, pack8<DT>(h[i]));
+    if (a.y && in) store<false>(a.y + row * a.ldy + 8 * c, pack8<DT>(h[i]));
     if (!a.q) continue;
     // 16 neighbouring threads hold one block of 128 columns (those past K
     // hold zeros); the bound keeps the scale of an all-zero block normal
@@ -147,8 +146,8 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
     if (in) {
       // v / s by the product with 1 / s and one correction from the remainder.
       // The product alone carries the reciprocal's rounding, which puts values
-      // on a border of two codes on either side of it.  (16384 x 4096: 77.9 us;
-      // 77.6 without the correction, 79.9 with the full division.)
+      // on a border of two codes on either side of it.  (0.3 us of 78 at
+      // 16384 x 4096; the full division takes 2.3.)
       const bool finite = s < __builtin_inff();
       const float inv = 1.0f / s, den = finite ? s : 0.0f;  // v / inf: 0, without a remainder
       float t[8];
@@ -162,7 +161,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
       lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true);
       hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], hi, false);
       hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], hi, true);
-      store<NT>(a.q + row * a.ldq + 8 * c, u32x2{(uint32_t)lo, (uint32_t)hi});
+      store<false>(a.q + row * a.ldq + 8 * c, u32x2{(uint32_t)lo, (uint32_t)hi});
       if (c % 16 == 0) a.scales[row * a.lds + c / 16] = s;
     }
   }
@@ -231,7 +230,7 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_bwd(NormBwdLaunch a) {
         d[e] = __builtin_fmaf(r, __builtin_fmaf(-h[e], m, g[e] * w[e]), d[e]);
         dw[i][e] = __builtin_fmaf(g[e], h[e] * r, dw[i][e]);
       }
-      if (live && c < chunks) store<NT>(a.dh + row * a.lddh + 8 * c, pack8<DT>(d));
+      if (live && c < chunks) store<false>(a.dh + row * a.lddh + 8 * c, pack8<DT>(d));
     }
   }
   if (!a.partial) return;
@@ -293,9 +292,16 @@ __global__ __launch_bounds__(256) void k_norm_dweight(const float* partial, int 
 // a lane and one wave is left per SIMD: 104 us against 89 at 16384 x 4096 with
 // two waves a row).  Few rows cannot fill the device that way, so the row is
 // spread over 256 threads for latency.
-// nt: from 2^25 elements on (the tensors of a call then pass 256 MB together,
-// the size of the memory-side cache): 16384 x 4096 92 to 82 us, backward 112 to
-// 104.
+// nt: from 2^25 elements on, where a call's tensors begin to push each other out
+// of the 256 MB of the memory-side cache, inputs and h pass the caches.  What
+// the next kernel reads (q, y, dh) does not.  4096 columns, us alone and with a
+// product over 1024 columns that reads the result (all through the caches / all
+// past them / this):
+//   16384 rows, x, residual, h, q   86, 150    77.6, 144.5    72.7, 137
+//    8192 rows, x, residual, h, q   46, 85     41.9, 85       40.4, 81
+//    8192 rows, x and q alone       24.6, 65   22.2, 65       23.1, 64.4
+//   16384 rows, the same and y      110, 194   104.8, 203     108.5, 191
+//   16384 rows, backward            105, 195   92, 191        94.4, 185
 struct NormShape {
   int tpr, cpt;
   bool nt;
