@@ -826,8 +826,12 @@ static hipError_t launch_tiled_grouped(const F8BlockLaunch& a, F8Lists* lists, h
 }
 
 hipError_t launch_f8_block_grouped(const F8BlockLaunch& a, void* workspace, hipStream_t stream) {
-  // few rows in all, or two a group on average: weights alone (128 experts, 128
-  // rows 59 us; with 16 experts and 256 rows the tiles take 31.6 against 40.9)
+  // Few rows in all, or two a group on average: weights alone.  How they are
+  // spread is known on the device only; 128 groups, N 2048, K 4096, us here and in
+  // tiles: 128 rows evenly 154 and 164, Zipf-skewed 66 and 69, in four groups 20
+  // and 29, in one 36 and 40; 256 rows 155 and 166, 96 and 108, 37 and 32, 65 and
+  // 54 (in two groups 66 and 40, the worst: a group's weights come once per 32
+  // rows).  More rows than two a group: 16 groups, 256 rows 41 and 32.
   if (a.M <= SK_ROWS || (a.M <= 2 * a.count && a.M <= 256)) return launch_skinny(a, stream);
   if (most_tiles(a, F8Large::UNIT) < device_cu_count())
     return launch_tiled_grouped<F8Small>(a, (F8Lists*)workspace, stream);
