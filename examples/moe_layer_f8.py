@@ -3,7 +3,9 @@
   forward   residual add + RMS norm -> fp8 rows with scales; router -> experts, weights, row order, balance loss;
             rows gathered by expert; up and gate projection per expert; SiLU; down projection per expert;
             weighted sum of each token's experts
-  backward  of the routing weights, the balance loss and the norm (the experts' weights are frozen)
+  backward  of the routing weights, the balance loss and the norm, and with through_experts of the experts' input, the
+            layer's whole data gradient: the same grouped products with the transposed weights, on gradients that are
+            quantised as activations are (the experts' weights are frozen)
 
     python examples/moe_layer_f8.py [--tokens 4096] [--hidden 4096] [--inner 1024] [--experts 128] [--top 8]
 """
@@ -39,6 +41,11 @@ def quantize_weight(w):
     return q.to(F8), s
 
 
+def transposed(w, s):
+    """The weights of the data gradient: codes and block scales of [experts][N][K] as those of [experts][K][N]."""
+    return w.view(torch.uint8).transpose(1, 2).contiguous().view(F8), s.transpose(1, 2).contiguous()
+
+
 class Layer:
     """Weights of one layer: norm [hidden], router [experts][hidden], gate + up [experts][2 inner][hidden], down
     [experts][hidden][inner]."""
@@ -54,6 +61,7 @@ class Layer:
         self.router = randn(experts, hidden, std=hidden ** -0.5).bfloat16()
         self.up = quantize_weight(randn(experts, 2 * inner, hidden, std=hidden ** -0.5))
         self.down = quantize_weight(randn(experts, hidden, inner, std=inner ** -0.5))
+        self.up_t, self.down_t = transposed(*self.up), transposed(*self.down)
 
     def forward(self, x, residual, mask=None):
         """Returns the layer's output, the new residual stream and what the backward pass needs."""
@@ -70,17 +78,32 @@ class Layer:
         d = gmi.gemm_f8_block_grouped(r.offsets, aq, a_scales, *self.down)
         expert_out = torch.where(r.slot_row[..., None] >= 0, d[r.slot_row.clamp_min(0).long()].float(), 0.0)
         out = (expert_out * r.weights[..., None]).sum(1).to(x.dtype)
-        return out, h, (h, y, logits, r, expert_out, mask)
+        return out, h, (h, y, logits, r, expert_out, (mask, token, routed, a))
 
-    def backward(self, dout, dloss, saved, dh_out=None):
-        """Gradients of the sum before the norm (through the routing weights and the balance loss, and past the norm:
-        dh_out), of the norm's and of the router's weight."""
-        h, y, logits, r, expert_out, mask = saved
+    def backward(self, dout, dloss, saved, dh_out=None, through_experts=False):
+        """Gradients of the sum before the norm (through the routing weights and the balance loss, past the norm:
+        dh_out, and through the experts if asked), of the norm's and of the router's weight."""
+        h, y, logits, r, expert_out, rows = saved
         dweights = (expert_out * dout[:, None].float()).sum(2)
-        dlogits = gmi.moe_route_bwd(logits, r.indices, r.weights, r.offsets, r.live, dweights, dloss, mask=mask)
+        dlogits = gmi.moe_route_bwd(logits, r.indices, r.weights, r.offsets, r.live, dweights, dloss, mask=rows[0])
         dy = dlogits @ self.router
+        if through_experts:
+            dy = (dy.float() + self.experts_backward(dout, r, rows)).to(dy.dtype)
         dh, dnorm = gmi.rmsnorm_bwd(dy, h, self.norm, dres=dh_out)
         return dh, dnorm, dlogits.t().contiguous() @ y
+
+    def experts_backward(self, dout, r, rows):
+        """Gradient of the experts' input, float32 [tokens][hidden] (the roundings to fp8 have no derivative)."""
+        _, token, routed, a = rows
+        share = torch.where(routed, r.weights.view(-1)[r.row_slot.clamp_min(0).long()], 0.0)
+        q, s = quantize(dout[token].float() * share[:, None])
+        dact = gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.down_t).float()
+        gate, up = a[:, : self.inner].float(), a[:, self.inner:].float()
+        sig = torch.sigmoid(gate)
+        da = torch.cat([dact * up * sig * (1.0 + gate * (1.0 - sig)), dact * gate * sig], 1)
+        q, s = quantize(torch.where(routed[:, None], da, 0.0))
+        dx = gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.up_t)
+        return torch.where(r.slot_row[..., None] >= 0, dx[r.slot_row.clamp_min(0).long()].float(), 0.0).sum(1)
 
 
 def main():
@@ -95,7 +118,7 @@ def main():
 
     def step():
         out, h, saved = layer.forward(x, res)
-        return saved[3], layer.backward(dout, dloss, saved, dh_out=dout)
+        return saved[3], layer.backward(dout, dloss, saved, dh_out=dout, through_experts=True)
 
     for _ in range(3):
         r, _ = step()
