@@ -55,8 +55,9 @@ __device__ __forceinline__ F8BlockLaunch k_split(F8BlockLaunch a, int split) {
 // moves whole 128-byte lines of 8 rows, where loads into the instruction's
 // registers take each line in two halves.  X, in the L2 after the first
 // workgroup's reads, goes straight to registers.  Past the last k-block the
-// loads return zeros without memory traffic.  Bound by memory: 16 rows, 8192 x
-// 8192 12.4 us (5.5 TB/s, launch included); 128 experts, 128 rows 59 us (6.4).
+// loads return zeros without memory traffic.  Bound by memory: 128 experts, 128
+// rows 59 us (6.4 TB/s); 16 rows, 8192 x 8192 16.8 us (4.0, launch included), 12.4
+// where the memory-side cache holds the weights.
 // Two k-blocks per wave in flight; with three or four the loads only queue
 // (experts 81-85 us).
 template <int TM, int D, bool NT>

@@ -18,8 +18,8 @@
 // same result on every run.
 //
 // Bound by latency, not by bytes or arithmetic: 16384 tokens x 128 bf16 experts,
-// top 8, 8.0 us and 9.0 for the second launch (4 MB read in 0.8 at copy rate);
-// 16 tokens fp32 5.4 in one launch; backward 6.0 and, 777 x 60, 3.5 (an empty
+// top 8, 7.8 us and 8.6 for the second launch (4 MB read in 0.8 at copy rate);
+// 16 tokens fp32 5.5 in one launch; backward 6.3 and, 777 x 60, 3.5 (an empty
 // launch takes 2.5).
 #include <algorithm>
 

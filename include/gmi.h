@@ -420,7 +420,8 @@ gmi_status gmi_conv2d_dgrad_implicit(int32_t N, int32_t H, int32_t W, int32_t C,
  *   s = max(max |v| over the 128-column block, 448 * 2^-126) / 448
  *   q = e4m3(v / s)               (if q is given, with scales; nearest even)
  * One launch (per 2^22 rows), each input read once.  A row that holds a NaN or an infinity
- * (or whose sum of squares passes the fp32 range) follows fp32 arithmetic.
+ * (or whose sum of squares passes the fp32 range) follows fp32 arithmetic; a NaN
+ * among v stands in q and does not enter the block's maximum.
  *   rows      >= 0 (0 is a no-op); K in 1 .. 32768, a multiple of 8.
  *   x         [rows][ldx]; residual [rows][ldr] or NULL (then h = x).
  *   weight    [K], the type of x, 16-byte aligned.
