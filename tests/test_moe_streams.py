@@ -88,3 +88,38 @@ def test_calls_on_another_stream_beside_queued_work(gmi, as_handle):
         got = call(side.cuda_stream if as_handle else side)
         torch.cuda.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.contiguous().view(torch.uint8)) for a, b in zip(want, got)), i
+
+
+@pytest.mark.gpu
+def test_calls_on_a_forked_stream_in_a_graph(gmi):
+    # captured on one stream, run on another that joins the capture: outputs and workspaces from the graph's memory
+    gen = torch.Generator().manual_seed(51)
+    T, K, N, E, k = 200, 2048, 256, 8, 2
+    x, dy = (torch.randn(T, K, generator=gen).to(torch.bfloat16).to(dev()) for _ in range(2))
+    w = torch.ones(K, dtype=torch.bfloat16, device=dev())
+    logits = torch.randn(T, E, generator=gen).to(dev())
+    W = (torch.randn(N, K, generator=gen) * 100).clamp(-448, 448).to(ref.F8).to(dev())
+    ws = torch.full((2, 16), 0.01, device=dev())
+    assert gmi.lib().gmi_gemm_f8_block_workspace_bytes(T, N, K) > 0
+
+    def calls(st):
+        q, s = gmi.rmsnorm_quant(x, w, stream=st)
+        return [gmi.gemm_f8_block(q, s, W, ws, stream=st), *gmi.moe_route(logits, k, stream=st),
+                *gmi.rmsnorm_bwd(dy, x, w, stream=st)]
+
+    calls(None)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        held = calls(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for step in range(3):
+        x.copy_(torch.randn(T, K, generator=gen).to(torch.bfloat16))
+        logits.copy_(torch.randn(T, E, generator=gen))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = calls(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager)), f"replay {step}"
