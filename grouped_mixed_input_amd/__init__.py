@@ -120,6 +120,26 @@ def lib() -> ctypes.CDLL:
     L.gmi_moe_route.argtypes = [_i32, _i32, _i32, _p, _i64, ctypes.c_int, _p, _i32] + [_p] * 9 + [_sz, _p]
     L.gmi_moe_route_bwd.restype = ctypes.c_int
     L.gmi_moe_route_bwd.argtypes = [_i32, _i32, _i32, _p, _i64, ctypes.c_int, _p, _i32] + [_p] * 7 + [_i64, _p]
+    L.gmi_group_rows_workspace_bytes.restype = _sz
+    L.gmi_group_rows_workspace_bytes.argtypes = [_i32] * 2
+    L.gmi_group_rows.restype = ctypes.c_int
+    L.gmi_group_rows.argtypes = [_i32, _i32] + [_p] * 5 + [_sz, _p]
+    L.gmi_moe_permute.restype = ctypes.c_int
+    L.gmi_moe_permute.argtypes = [_i32, _i32, _i32, ctypes.c_int, _p, _i64, _p, _i64, _p, _i32, _p, _i64, _p, _i64, _p]
+    L.gmi_moe_unpermute.restype = ctypes.c_int
+    L.gmi_moe_unpermute.argtypes = [_i32, _i32, _i32, ctypes.c_int, _p, _i64, _i32, _p, _p, _p, _i64, _p, _i64, _p]
+    L.gmi_moe_unpermute_bwd.restype = ctypes.c_int
+    L.gmi_moe_unpermute_bwd.argtypes = [_i32, _i32, _i32, ctypes.c_int, _p, _i64, _p, _p, _p, _i64, _i32, _p, _i64, _p,
+                                        _i64, _p, _i64, _p, _p]
+    L.gmi_swiglu_quant.restype = ctypes.c_int
+    L.gmi_swiglu_quant.argtypes = [_i32, _i32, ctypes.c_int, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p]
+    L.gmi_swiglu_bwd.restype = ctypes.c_int
+    L.gmi_swiglu_bwd.argtypes = [_i32, _i32, ctypes.c_int, _p, _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p]
+    L.gmi_gemm_lora_workspace_bytes.restype = _sz
+    L.gmi_gemm_lora_workspace_bytes.argtypes = [_i32] * 4
+    L.gmi_gemm_lora.restype = ctypes.c_int
+    L.gmi_gemm_lora.argtypes = [_i32] * 5 + [ctypes.c_int, _p, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p,
+                                             _i64, _p, _i64, _p, _sz, _p]
     _lib = L
     return L
 
@@ -133,6 +153,19 @@ def _stream(stream) -> int:
     if stream is None:  # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_on(stream, device: int) -> int:
+    """The stream of a call whose tensors are on `device`: a kernel is launched on the current device."""
+    current = torch._C._cuda_getDevice()
+    if device != current:
+        raise ValueError(f"the tensors are on device {device}, the current one is {current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(current)
+    at = getattr(stream, "device_index", None)
+    if at is not None and at != device:
+        raise ValueError(f"the tensors are on device {device}, the stream on {at}")
+    return _stream(stream)
 
 
 def _ptr(t) -> int | None:
@@ -439,6 +472,9 @@ def _bound():
         native.bind(*(ctypes.cast(f, _p).value for f in (
             L.gmi_rmsnorm_quant, L.gmi_rmsnorm_bwd, L.gmi_gemm_f8_block, L.gmi_gemm_f8_block_grouped, L.gmi_moe_route,
             L.gmi_moe_route_bwd)), _stream)
+        native.bind_rows(*(ctypes.cast(f, _p).value for f in (
+            L.gmi_group_rows, L.gmi_moe_permute, L.gmi_moe_unpermute, L.gmi_moe_unpermute_bwd, L.gmi_swiglu_quant,
+            L.gmi_swiglu_bwd, L.gmi_gemm_lora)), _stream_on)
         _native = native
     return _native
 
@@ -562,3 +598,132 @@ def moe_route_bwd(logits: torch.Tensor, indices: torch.Tensor, weights: torch.Te
     _check(_bound().moe_route_bwd(logits, indices, weights, offsets, live, dweights, dloss, mask, renormalize, dlogits,
                                   stream))
     return dlogits
+
+
+# ---------------------------------------------------------------- rows between the experts' products
+class Grouping(NamedTuple):
+    """What group_rows writes, int32: the row offsets [groups + 1], the rows by group [n] (those of no group last) and
+    each row's place among them, in the shape of the index (-1 for rows of no group)."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    place: torch.Tensor
+
+
+def group_rows(index: torch.Tensor, groups: int, out: Grouping | None = None, workspace: torch.Tensor | None = None,
+               stream=None) -> Grouping:
+    """Rows ordered by the number that each carries: `index` int32, of any shape, its rows counted in memory order; see
+    Grouping.  With the experts of a router's slots [tokens][k] as index, offsets, order and place serve as moe_route's
+    offsets, row_slot and slot_row; with the adapters of a batch's rows, order is that of gemm_lora.  A row whose
+    number lies outside [0, groups) belongs to no group."""
+    if out is None:
+        n, dev, i32 = index.numel(), index.device, torch.int32
+        out = Grouping(_new((groups + 1,), i32, dev, stream), _new((n,), i32, dev, stream),
+                       _new(index.shape, i32, dev, stream))
+    if workspace is None:
+        workspace = _scratch(lib().gmi_group_rows_workspace_bytes(index.numel(), groups), index.device, stream)
+    _check(_bound().group_rows(index, groups, *out, workspace, stream))
+    return out
+
+
+def moe_permute(x: torch.Tensor, slot_row: torch.Tensor, scales: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, out_scales: torch.Tensor | None = None, stream=None):
+    """Each token's row copied to the rows of its slots: out[slot_row[t, i]] = x[t].  x [tokens][K] float16, bfloat16 or
+    float8_e4m3fn, the last with its `scales` float32 [tokens][ceil(K / 128)] where given; slot_row int32 [tokens][k]
+    as moe_route writes it.  Returns out [tokens * k][K] (or as given), with scales (out, out_scales).  Rows that no
+    slot has are not written.  The gradient is moe_unpermute without weights."""
+    rows = slot_row.numel() if out is None else out.shape[0]
+    if out is None:
+        out = _new((rows, x.shape[1]), x.dtype, x.device, stream)
+    if scales is not None and out_scales is None:
+        out_scales = _new((rows, scales.shape[1]), torch.float32, x.device, stream)
+    _check(_bound().moe_permute(x, slot_row, scales, out, out_scales, stream))
+    return out if scales is None else (out, out_scales)
+
+
+def moe_unpermute(rows: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor | None = None,
+                  add: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = add[t] + sum_i weights[t, i] * rows[slot_row[t, i]], summed in float32 and rounded once: the experts'
+    rows [n][K] (float16 or bfloat16) back to the tokens.  `weights` float32 [tokens][k] (None: 1), `add` [tokens][K]
+    in the rows' type (out may be add).  Slots without a row add nothing."""
+    if out is None:
+        out = _new((slot_row.shape[0], rows.shape[1]), rows.dtype, rows.device, stream)
+    _check(_bound().moe_unpermute(rows, slot_row, weights, add, out, stream))
+    return out
+
+
+def moe_unpermute_bwd(dout: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor | None = None,
+                      rows: torch.Tensor | None = None, drows: torch.Tensor | None = None,
+                      scales: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
+                      quantize: bool = False, stream=None):
+    """Gradients of moe_unpermute: drows[slot_row[t, i]] = weights[t, i] * dout[t], in dout's type or with
+    quantize=True as float8_e4m3fn with `scales` float32 [n][ceil(K / 128)], and dweights[t, i] = <dout[t],
+    rows[slot_row[t, i]]> float32 where `rows` (what the forward call read) is given.  Returns (drows, dweights), or
+    (drows, scales, dweights) with quantize; dweights is None without rows.  Rows that no slot has are not written."""
+    if rows is None and dweights is not None:
+        raise ValueError("dweights needs the rows of the forward call")
+    if scales is not None and not quantize:
+        raise ValueError("scales are written with quantize=True only")
+    n = slot_row.numel() if rows is None else rows.shape[0]
+    if drows is None:
+        drows = _new((n, dout.shape[1]), torch.float8_e4m3fn if quantize else dout.dtype, dout.device, stream)
+    if quantize and scales is None:
+        scales = _new((drows.shape[0], _scale_blocks(dout.shape[1])), torch.float32, dout.device, stream)
+    if rows is not None and dweights is None:
+        dweights = _new(slot_row.shape, torch.float32, dout.device, stream)
+    _check(_bound().moe_unpermute_bwd(dout, slot_row, weights, rows, None if quantize else drows,
+                                      drows if quantize else None, scales, dweights, stream))
+    return (drows, scales, dweights) if quantize else (drows, dweights)
+
+
+def swiglu_quant(a: torch.Tensor, live: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                 q: torch.Tensor | None = None, scales: torch.Tensor | None = None, quantize: bool = True, stream=None):
+    """v = silu(gate) * up of a [rows][2 N] (gate first; float16 or bfloat16) between an expert's two products: q =
+    e4m3(v / s) with one float32 scale s per row and 128 columns; `y` (v in a's type) is written where given.  `live`
+    (int32 [1] on the device: offsets[-1:] of the routing) leaves the rows from there on alone.  Returns (q, scales);
+    with quantize=False only `y` (made if not given) is written and returned."""
+    rows, N = a.shape[0], a.shape[1] // 2
+    if quantize:
+        if q is None:
+            q = _new((rows, N), torch.float8_e4m3fn, a.device, stream)
+        if scales is None:
+            scales = _new((rows, _scale_blocks(N)), torch.float32, a.device, stream)
+    elif q is not None or scales is not None:
+        raise ValueError("q and scales are written with quantize=True only")
+    elif y is None:
+        y = _new((rows, N), a.dtype, a.device, stream)
+    _check(_bound().swiglu_quant(a, live, y, q, scales, stream))
+    return (q, scales) if quantize else y
+
+
+def swiglu_bwd(dact: torch.Tensor, a: torch.Tensor, live: torch.Tensor | None = None, da: torch.Tensor | None = None,
+               scales: torch.Tensor | None = None, quantize: bool = False, stream=None):
+    """Gradient of swiglu_quant's v: da [rows][2 N], that of the gate first, from `dact` [rows][N] and the forward's
+    `a`; in a's type (da may be a), or with quantize=True as float8_e4m3fn with `scales` float32
+    [rows][ceil(2 N / 128)].  Returns da, or (da, scales)."""
+    if scales is not None and not quantize:
+        raise ValueError("scales are written with quantize=True only")
+    if da is None:
+        da = _new(a.shape, torch.float8_e4m3fn if quantize else a.dtype, a.device, stream)
+    if quantize and scales is None:
+        scales = _new((a.shape[0], _scale_blocks(a.shape[1])), torch.float32, a.device, stream)
+    _check(_bound().swiglu_bwd(dact, a, live, None if quantize else da, da if quantize else None, scales, stream))
+    return (da, scales) if quantize else da
+
+
+# ---------------------------------------------------------------- adapters
+def gemm_lora(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, index: torch.Tensor,
+              scales: torch.Tensor | None = None, order: torch.Tensor | None = None, base: torch.Tensor | None = None,
+              Y: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[m] = base[m] + scales[a] * (X[m] A[a]^T) B[a]^T with a = index[m]: low-rank adapters of many requests beside one
+    dense product, whose result is `base` (Y may be base; None: zeros).  X [M][K], A [adapters][rank][K], B
+    [adapters][N][rank], base and Y [M][N] share one type, float16 or bfloat16; index int32 [M], -1 for rows without an
+    adapter; scales float32 [adapters] (None: 1).  `order` (int32 [M], group_rows(index, adapters).order) brings rows
+    of one adapter together, for speed: rows in any order give the same results.  `workspace`: a device byte tensor of
+    lib().gmi_gemm_lora_workspace_bytes(M, N, K, rank) bytes; made for the call if not given."""
+    if Y is None:
+        Y = _new((X.shape[0], B.shape[1]), X.dtype, X.device, stream)
+    if workspace is None:
+        need = lib().gmi_gemm_lora_workspace_bytes(X.shape[0], B.shape[1], X.shape[1], A.shape[1])
+        workspace = _scratch(need, X.device, stream)
+    _check(_bound().gemm_lora(X, A, B, index, scales, order, base, Y, workspace, stream))
+    return Y

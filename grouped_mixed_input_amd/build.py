@@ -17,7 +17,7 @@ LIB = PKG / "libgmi.so"
 CALLS = PKG / "_calls.so"
 OBJDIR = PKG / "_build"
 SOURCES = ["gmi_api.hip", "kernels_gemm.hip", "kernels_conv.hip", "kernels_w4a16.hip", "kernels_norm.hip",
-           "kernels_f8block.hip", "kernels_route.hip"]
+           "kernels_f8block.hip", "kernels_route.hip", "kernels_rows.hip", "kernels_lora.hip"]
 ARCH = "gfx950"
 
 

@@ -1072,4 +1072,323 @@ gmi_status gmi_moe_route_bwd(int32_t tokens, int32_t experts, int32_t k, const v
   return hip_status(launch_route_bwd(a, (int)dtype, (hipStream_t)stream), who);
 }
 
+// ---------------------------------------------------------------------------
+// rows between the products of a mixture-of-experts layer
+// ---------------------------------------------------------------------------
+// whether p is aligned to n bytes (a power of two)
+static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// a [rows][ld] operand of 16-byte accesses whose rows hold `cols` elements, ld a multiple of `unit`
+static gmi_status row_operand(const char* who, const char* name, const void* p, int64_t ld, int64_t cols, int unit = 8) {
+  if (!p) return fail(GMI_ERR_INVALID_ARG, "%s: %s is NULL", who, name);
+  if (ld < cols) return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension of %s below its row width", who, name);
+  if (!aligned16(p) || ld % unit)
+    return fail(GMI_ERR_MISALIGNED, "%s: %s must be 16-byte aligned, its leading dimension a multiple of %d", who, name,
+                unit);
+  return GMI_OK;
+}
+// codes [rows][ldq] of `cols` columns with their scales [rows][lds]
+static gmi_status code_operand(const char* who, const void* q, int64_t ldq, const float* scales, int64_t lds,
+                               int64_t cols) {
+  if (!q || !scales) return fail(GMI_ERR_INVALID_ARG, "%s: q and scales go together", who);
+  if (ldq < cols || lds < cdiv(cols, 128))
+    return fail(GMI_ERR_INVALID_ARG, "%s: leading dimension of q or scales below its row width", who);
+  if (!aligned(q, 8) || ldq % 8 || !aligned(scales, 4))
+    return fail(GMI_ERR_MISALIGNED, "%s: q must be 8-byte aligned, ldq a multiple of 8, scales 4-byte aligned", who);
+  return GMI_OK;
+}
+
+size_t gmi_group_rows_workspace_bytes(int32_t n, int32_t groups) {
+  if (n <= 0 || groups < 1 || groups > kMaxGroups || n > INT32_MAX - (1 << 17)) return 0;
+  return plan_group(n, groups).bytes;
+}
+
+gmi_status gmi_group_rows(int32_t n, int32_t groups, const int32_t* index, int32_t* offsets, int32_t* order,
+                          int32_t* place, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const char* who = "group_rows";
+  if (n < 0 || groups < 1) return fail(GMI_ERR_INVALID_ARG, "%s: n %d < 0 or groups %d < 1", who, n, groups);
+  if (groups > kMaxGroups) return fail(GMI_ERR_UNSUPPORTED, "%s: %d groups, at most %d", who, groups, kMaxGroups);
+  if (n > INT32_MAX - (1 << 17)) return fail(GMI_ERR_UNSUPPORTED, "%s: n not below 2^31 - 2^17", who);
+  if (!offsets || (n > 0 && (!index || !order || !place))) return fail(GMI_ERR_INVALID_ARG, "%s: a NULL operand", who);
+  if (!aligned(index, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(place, 4))
+    return fail(GMI_ERR_MISALIGNED, "%s: operands must be 4-byte aligned", who);
+  const size_t need = gmi_group_rows_workspace_bytes(n, groups);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+  if (need && !aligned16(workspace)) return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
+  GroupLaunch a{};
+  a.index = index;
+  a.n = n;
+  a.G = groups;
+  a.offsets = offsets;
+  a.order = order;
+  a.place = place;
+  return hip_status(launch_group(a, workspace, (hipStream_t)stream), who);
+}
+
+// sizes shared by the calls that move tokens to their experts' rows and back
+static gmi_status slot_sizes(const char* who, int32_t tokens, int32_t k, int32_t K, int32_t rows, gmi_dtype dtype,
+                             bool f8) {
+  if (tokens < 0 || k < 1 || K < 1 || rows < 0)
+    return fail(GMI_ERR_INVALID_ARG, "%s: tokens %d, k %d, K %d, rows %d", who, tokens, k, K, rows);
+  if (k > kMaxTopK) return fail(GMI_ERR_UNSUPPORTED, "%s: k %d above %d", who, k, kMaxTopK);
+  if ((int64_t)tokens * k > INT32_MAX - (1 << 17))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: tokens * k not below 2^31 - 2^17", who);
+  if (!dtype_ok(dtype) && !(f8 && dtype == GMI_F8E4M3))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
+  const int unit = dtype == GMI_F8E4M3 ? 16 : 8;
+  if (K % unit) return fail(GMI_ERR_MISALIGNED, "%s: K must be a multiple of %d (128-bit accesses)", who, unit);
+  return GMI_OK;
+}
+static gmi_status slot_rows(const char* who, const int32_t* slot_row) {
+  if (!slot_row) return fail(GMI_ERR_INVALID_ARG, "%s: slot_row is NULL", who);
+  if (!aligned(slot_row, 4)) return fail(GMI_ERR_MISALIGNED, "%s: slot_row must be 4-byte aligned", who);
+  return GMI_OK;
+}
+
+gmi_status gmi_moe_permute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* x, int64_t ldx,
+                           const float* x_scales, int64_t ldxs, const int32_t* slot_row, int32_t rows, void* out,
+                           int64_t ldo, float* out_scales, int64_t ldos, void* stream) {
+  g_last_error.clear();
+  const char* who = "moe_permute";
+  gmi_status st = slot_sizes(who, tokens, k, K, rows, dtype, true);
+  if (st != GMI_OK || tokens == 0 || rows == 0) return st;
+  const bool f8 = dtype == GMI_F8E4M3;
+  const int unit = f8 ? 16 : 8, size = f8 ? 1 : 2;
+  if ((st = row_operand(who, "x", x, ldx, K, unit)) != GMI_OK || (st = slot_rows(who, slot_row)) != GMI_OK ||
+      (st = row_operand(who, "out", out, ldo, K, unit)) != GMI_OK)
+    return st;
+  if ((x_scales == nullptr) != (out_scales == nullptr))
+    return fail(GMI_ERR_INVALID_ARG, "%s: x_scales and out_scales go together", who);
+  if (x_scales && !f8) return fail(GMI_ERR_INVALID_ARG, "%s: scales belong to fp8 rows", who);
+  if (x_scales && (ldxs < cdiv(K, 128) || ldos < cdiv(K, 128)))
+    return fail(GMI_ERR_INVALID_ARG, "%s: a leading dimension of scales below ceil(K / 128)", who);
+  if (!aligned(x_scales, 4) || !aligned(out_scales, 4))
+    return fail(GMI_ERR_MISALIGNED, "%s: scales must be 4-byte aligned", who);
+  PermuteLaunch a{};
+  a.x = (const char*)x;
+  a.x_scales = x_scales;
+  a.slot_row = slot_row;
+  a.out = (char*)out;
+  a.out_scales = out_scales;
+  a.T = tokens;
+  a.ldx = ldx * size;
+  a.ldo = ldo * size;
+  a.ldxs = ldxs;
+  a.ldos = ldos;
+  a.k = k;
+  a.rows = rows;
+  a.chunks = K / unit;
+  a.blocks = x_scales ? (int)cdiv(K, 128) : 0;
+  return hip_status(launch_permute(a, (hipStream_t)stream), who);
+}
+
+gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* y, int64_t ldy,
+                             int32_t rows, const int32_t* slot_row, const float* weights, const void* add,
+                             int64_t ldadd, void* out, int64_t ldo, void* stream) {
+  g_last_error.clear();
+  const char* who = "moe_unpermute";
+  gmi_status st = slot_sizes(who, tokens, k, K, rows, dtype, false);
+  if (st != GMI_OK || tokens == 0) return st;
+  if ((rows > 0 && (st = row_operand(who, "y", y, ldy, K)) != GMI_OK) ||
+      (st = slot_rows(who, slot_row)) != GMI_OK || (add && (st = row_operand(who, "add", add, ldadd, K)) != GMI_OK) ||
+      (st = row_operand(who, "out", out, ldo, K)) != GMI_OK)
+    return st;
+  if (!aligned(weights, 4)) return fail(GMI_ERR_MISALIGNED, "%s: weights must be 4-byte aligned", who);
+  UnpermuteLaunch a{};
+  a.y = (const uint16_t*)y;
+  a.add = (const uint16_t*)add;
+  a.slot_row = slot_row;
+  a.weights = weights;
+  a.out = (uint16_t*)out;
+  a.T = tokens;
+  a.ldy = ldy;
+  a.lda = ldadd;
+  a.ldo = ldo;
+  a.k = k;
+  a.rows = rows;
+  a.chunks = K / 8;
+  return hip_status(launch_unpermute(a, (int)dtype, (hipStream_t)stream), who);
+}
+
+gmi_status gmi_moe_unpermute_bwd(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* dout,
+                                 int64_t lddout, const int32_t* slot_row, const float* weights, const void* y,
+                                 int64_t ldy, int32_t rows, void* drows, int64_t lddrows, void* q, int64_t ldq,
+                                 float* scales, int64_t lds, float* dweights, void* stream) {
+  g_last_error.clear();
+  const char* who = "moe_unpermute_bwd";
+  gmi_status st = slot_sizes(who, tokens, k, K, rows, dtype, false);
+  if (st != GMI_OK || tokens == 0) return st;
+  if ((st = row_operand(who, "dout", dout, lddout, K)) != GMI_OK || (st = slot_rows(who, slot_row)) != GMI_OK)
+    return st;
+  if ((drows == nullptr) == (q == nullptr && scales == nullptr) && rows > 0)
+    return fail(GMI_ERR_INVALID_ARG, "%s: either drows or q with scales", who);
+  if (rows > 0 && (drows ? (st = row_operand(who, "drows", drows, lddrows, K)) : (st = code_operand(who, q, ldq, scales, lds, K))) != GMI_OK)
+    return st;
+  if (dweights && rows > 0 && (st = row_operand(who, "y", y, ldy, K)) != GMI_OK) return st;
+  if (!aligned(weights, 4) || !aligned(dweights, 4))
+    return fail(GMI_ERR_MISALIGNED, "%s: weights and dweights must be 4-byte aligned", who);
+  if (rows == 0 && !dweights) return GMI_OK;
+  UnpermuteBwdLaunch a{};
+  a.dout = (const uint16_t*)dout;
+  a.y = dweights ? (const uint16_t*)y : nullptr;
+  a.slot_row = slot_row;
+  a.weights = weights;
+  a.drows = (uint16_t*)drows;
+  a.q = (uint8_t*)q;
+  a.scales = scales;
+  a.dweights = dweights;
+  a.T = tokens;
+  a.ldd = lddout;
+  a.ldy = ldy;
+  a.lddr = lddrows;
+  a.ldq = ldq;
+  a.lds = lds;
+  a.k = k;
+  a.rows = rows;
+  a.chunks = K / 8;
+  return hip_status(launch_unpermute_bwd(a, (int)dtype, (hipStream_t)stream), who);
+}
+
+static gmi_status swiglu_sizes(const char* who, int32_t rows, int32_t N, gmi_dtype dtype, const int32_t* live) {
+  if (rows < 0 || N < 1) return fail(GMI_ERR_INVALID_ARG, "%s: rows %d < 0 or N %d < 1", who, rows, N);
+  if (!dtype_ok(dtype)) return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
+  if (N > (1 << 22)) return fail(GMI_ERR_UNSUPPORTED, "%s: N above 2^22", who);
+  if (N % 8) return fail(GMI_ERR_MISALIGNED, "%s: N must be a multiple of 8 (128-bit accesses)", who);
+  if (!aligned(live, 4)) return fail(GMI_ERR_MISALIGNED, "%s: live must be 4-byte aligned", who);
+  return GMI_OK;
+}
+
+gmi_status gmi_swiglu_quant(int32_t rows, int32_t N, gmi_dtype dtype, const void* a_, int64_t lda, const int32_t* live,
+                            void* y, int64_t ldy, void* q, int64_t ldq, float* scales, int64_t lds, void* stream) {
+  g_last_error.clear();
+  const char* who = "swiglu_quant";
+  gmi_status st = swiglu_sizes(who, rows, N, dtype, live);
+  if (st != GMI_OK || rows == 0) return st;
+  if (!y && !q && !scales) return fail(GMI_ERR_INVALID_ARG, "%s: neither y nor q is wanted", who);
+  if ((st = row_operand(who, "a", a_, lda, 2 * (int64_t)N)) != GMI_OK ||
+      (y && (st = row_operand(who, "y", y, ldy, N)) != GMI_OK) ||
+      ((q || scales) && (st = code_operand(who, q, ldq, scales, lds, N)) != GMI_OK))
+    return st;
+  SwigluLaunch a{};
+  a.rows = rows;
+  a.N = N;
+  a.a = (const uint16_t*)a_;
+  a.live = live;
+  a.y = (uint16_t*)y;
+  a.q = (uint8_t*)q;
+  a.scales = scales;
+  a.lda = lda;
+  a.ldy = ldy;
+  a.ldq = ldq;
+  a.lds = lds;
+  return hip_status(launch_swiglu(a, (int)dtype, (hipStream_t)stream), who);
+}
+
+gmi_status gmi_swiglu_bwd(int32_t rows, int32_t N, gmi_dtype dtype, const void* dact, int64_t lddact, const void* a_,
+                          int64_t lda, const int32_t* live, void* da, int64_t ldda, void* q, int64_t ldq, float* scales,
+                          int64_t lds, void* stream) {
+  g_last_error.clear();
+  const char* who = "swiglu_bwd";
+  gmi_status st = swiglu_sizes(who, rows, N, dtype, live);
+  if (st != GMI_OK || rows == 0) return st;
+  if ((da == nullptr) == (q == nullptr && scales == nullptr))
+    return fail(GMI_ERR_INVALID_ARG, "%s: either da or q with scales", who);
+  if ((st = row_operand(who, "dact", dact, lddact, N)) != GMI_OK ||
+      (st = row_operand(who, "a", a_, lda, 2 * (int64_t)N)) != GMI_OK ||
+      (st = da ? row_operand(who, "da", da, ldda, 2 * (int64_t)N)
+               : code_operand(who, q, ldq, scales, lds, 2 * (int64_t)N)) != GMI_OK)
+    return st;
+  SwigluLaunch a{};
+  a.rows = rows;
+  a.N = N;
+  a.a = (const uint16_t*)a_;
+  a.dact = (const uint16_t*)dact;
+  a.live = live;
+  a.y = (uint16_t*)da;
+  a.q = (uint8_t*)q;
+  a.scales = scales;
+  a.lda = lda;
+  a.ldd = lddact;
+  a.ldy = ldda;
+  a.ldq = ldq;
+  a.lds = lds;
+  return hip_status(launch_swiglu_bwd(a, (int)dtype, (hipStream_t)stream), who);
+}
+
+// ---------------------------------------------------------------------------
+// low-rank adapters beside a dense product
+// ---------------------------------------------------------------------------
+constexpr int32_t kMaxLoraRows = int32_t(1) << 29;  // a launch's threads stay below 2^32
+
+size_t gmi_gemm_lora_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t rank) {
+  if (M <= 0 || N <= 0 || K <= 0 || rank <= 0 || rank > kMaxLoraRank || M > kMaxLoraRows) return 0;
+  return lora_workspace(M, K, rank);
+}
+
+gmi_status gmi_gemm_lora(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters, gmi_dtype dtype,
+                         const void* X, int64_t ldx, const void* A, int64_t lda, int64_t a_stride, const void* B,
+                         int64_t ldb, int64_t b_stride, const float* scales, const int32_t* index,
+                         const int32_t* order, const void* base, int64_t ldbase, void* Y, int64_t ldy,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const char* who = "gemm_lora";
+  if (M < 0 || N < 0 || K < 1 || rank < 1 || adapters < 0)
+    return fail(GMI_ERR_INVALID_ARG, "%s: M %d, N %d, K %d, rank %d, adapters %d", who, M, N, K, rank, adapters);
+  if (!dtype_ok(dtype)) return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
+  if (rank > kMaxLoraRank) return fail(GMI_ERR_UNSUPPORTED, "%s: rank %d above %d", who, rank, kMaxLoraRank);
+  if (M > kMaxLoraRows) return fail(GMI_ERR_UNSUPPORTED, "%s: M above 2^29", who);
+  if (N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+    return fail(GMI_ERR_UNSUPPORTED, "%s: N or K not below 2^31 - 2^10", who);
+  if (N % 8 || K % 8 || rank % 8)
+    return fail(GMI_ERR_MISALIGNED, "%s: N, K and rank must be multiples of 8 (128-bit accesses)", who);
+  if (M == 0 || N == 0) return GMI_OK;
+  gmi_status st;
+  if ((st = row_operand(who, "X", X, ldx, K)) != GMI_OK ||
+      (base && (st = row_operand(who, "base", base, ldbase, N)) != GMI_OK) ||
+      (st = row_operand(who, "Y", Y, ldy, N)) != GMI_OK)
+    return st;
+  if (base == Y && ldbase != ldy)
+    return fail(GMI_ERR_INVALID_ARG, "%s: Y may be base only with its leading dimension", who);
+  if (adapters > 0) {
+    if ((st = row_operand(who, "A", A, lda, K)) != GMI_OK || (st = row_operand(who, "B", B, ldb, rank)) != GMI_OK)
+      return st;
+    if (a_stride % 8 || b_stride % 8)
+      return fail(GMI_ERR_MISALIGNED, "%s: a_stride and b_stride must be multiples of 8", who);
+    if (adapters > 1 && (a_stride < (rank - 1) * lda + K || b_stride < (N - 1) * ldb + rank))
+      return fail(GMI_ERR_INVALID_ARG, "%s: an adapter stride is smaller than one adapter's data", who);
+  }
+  if (!index) return fail(GMI_ERR_INVALID_ARG, "%s: index is NULL", who);
+  if (!aligned(index, 4) || !aligned(order, 4) || !aligned(scales, 4))
+    return fail(GMI_ERR_MISALIGNED, "%s: index, order and scales must be 4-byte aligned", who);
+  const size_t need = lora_workspace(M, K, rank);
+  if (!workspace || workspace_bytes < need)
+    return fail(GMI_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(GMI_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", who);
+  LoraLaunch a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.rank = rank;
+  a.adapters = adapters;
+  a.X = (const uint16_t*)X;
+  a.A = (const uint16_t*)A;
+  a.B = (const uint16_t*)B;
+  a.base = (const uint16_t*)base;
+  a.scales = scales;
+  a.index = index;
+  a.order = order;
+  a.Y = (uint16_t*)Y;
+  a.ldx = ldx;
+  a.lda = lda;
+  a.a_stride = a_stride;
+  a.ldb = ldb;
+  a.b_stride = b_stride;
+  a.ldbase = ldbase;
+  a.ldy = ldy;
+  a.part = (float*)workspace;
+  return hip_status(launch_lora(a, (int)dtype, (hipStream_t)stream), who);
+}
+
 }  // extern "C"

@@ -252,4 +252,88 @@ RoutePlan plan_route(int T, int E);
 hipError_t launch_route(const RouteLaunch& a, int dtype, void* workspace, hipStream_t stream);
 hipError_t launch_route_bwd(const RouteBwdLaunch& a, int dtype, hipStream_t stream);
 
+// Rows ordered by a number that each carries
+struct GroupLaunch {
+  const int32_t* index;
+  int n, G;
+  int32_t *offsets, *order, *place;
+  int rows_per_wg;
+  uint16_t* wg_counts;  // several workgroups: their rows per group
+};
+struct GroupPlan {
+  int wgs, rows_per_wg;
+  size_t bytes;  // workspace (0 with one workgroup)
+};
+constexpr int kMaxGroups = 1024;
+GroupPlan plan_group(int n, int G);
+hipError_t launch_group(const GroupLaunch& a, void* workspace, hipStream_t stream);
+
+// Tokens to their experts' rows and back.  Leading dimensions in elements,
+// except those of the permutation, which copies bytes.
+struct PermuteLaunch {
+  const char* x;
+  const float* x_scales;
+  const int32_t* slot_row;
+  char* out;
+  float* out_scales;
+  int64_t T, ldx, ldo, ldxs, ldos;
+  int k, rows, chunks, blocks;  // chunks of 16 bytes; blocks: scales a row (0: none)
+  int shift;                    // 2^shift waves a token, `waves` in all
+  int64_t waves;
+};
+struct UnpermuteLaunch {
+  const uint16_t *y, *add;
+  const int32_t* slot_row;
+  const float* weights;
+  uint16_t* out;
+  int64_t T, ldy, lda, ldo;
+  int k, rows, chunks;  // chunks of 8 columns
+  int shift;
+  int64_t waves;
+};
+struct UnpermuteBwdLaunch {
+  const uint16_t *dout, *y;
+  const int32_t* slot_row;
+  const float* weights;
+  uint16_t* drows;
+  uint8_t* q;  // instead of drows, with scales
+  float *scales, *dweights;
+  int64_t T, ldd, ldy, lddr, ldq, lds;
+  int k, rows, chunks;
+};
+hipError_t launch_permute(const PermuteLaunch& a, hipStream_t stream);
+hipError_t launch_unpermute(const UnpermuteLaunch& a, int dtype, hipStream_t stream);
+hipError_t launch_unpermute_bwd(const UnpermuteBwdLaunch& a, int dtype, hipStream_t stream);
+
+// Gated activation: a holds gate and up side by side, N columns each.  The
+// gradient takes dact and writes 2 N columns, in 16 bits (y) or as codes (q).
+struct SwigluLaunch {
+  int64_t rows;
+  int N;
+  const uint16_t *a, *dact;
+  const int32_t* live;  // rows in use, on the device (NULL: all); row0 of them lie before this launch's
+  int64_t row0;
+  uint16_t* y;
+  uint8_t* q;
+  float* scales;
+  int64_t lda, ldd, ldy, ldq, lds;
+};
+hipError_t launch_swiglu(const SwigluLaunch& a, int dtype, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwigluLaunch& a, int dtype, hipStream_t stream);
+
+// Y = base + s (X A^T) B^T, each row with the adapter index[row]
+struct LoraLaunch {
+  int M, N, K, rank, adapters;
+  const uint16_t *X, *A, *B, *base;
+  const float* scales;   // NULL: 1
+  const int32_t *index, *order;  // order NULL: rows as they come
+  uint16_t* Y;
+  int64_t ldx, lda, a_stride, ldb, b_stride, ldbase, ldy;
+  float* part;  // [splits][M][rank]: X A^T over runs of K, rows in the order of the call
+  int splits;
+};
+constexpr int kMaxLoraRank = 128;
+size_t lora_workspace(int M, int K, int rank);
+hipError_t launch_lora(const LoraLaunch& a, int dtype, hipStream_t stream);
+
 }  // namespace gmi

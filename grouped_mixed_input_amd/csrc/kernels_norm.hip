@@ -18,30 +18,9 @@
 // 2.5 us, an empty launch's time.
 #include "gmi_device.hpp"
 #include "gmi_internal.hpp"
+#include "gmi_rows.hpp"
 
 namespace gmi {
-
-// max / sum over aligned groups of 16 lanes, result in every lane (quad swaps
-// then half-row and row mirrors: four DPP moves, no LDS)
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
-}
-__device__ __forceinline__ float max16(float v) {
-  v = fmaxf(v, dpp<0xB1>(v));
-  v = fmaxf(v, dpp<0x4E>(v));
-  v = fmaxf(v, dpp<0x141>(v));
-  return fmaxf(v, dpp<0x140>(v));
-}
-__device__ __forceinline__ float sum64(float v) {
-  v += dpp<0xB1>(v);
-  v += dpp<0x4E>(v);
-  v += dpp<0x141>(v);
-  v += dpp<0x140>(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
 
 // Sum over the team of TPR threads that share a row.  `red` holds one float
 // per wave of the workgroup; two barriers, so that the next call may reuse it.
@@ -59,35 +38,6 @@ __device__ __forceinline__ float team_sum(float v, float* red) {
     __syncthreads();
   }
   return v;
-}
-
-template <int DT>
-__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = from_bits<DT>(v[i] & 0xffffu);
-    f[2 * i + 1] = from_bits<DT>(v[i] >> 16);
-  }
-}
-template <int DT>
-__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
-  return u32x4{pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7])};
-}
-
-constexpr float kF8Max = 448.0f;
-
-// One 16-byte access, or past the caches (NT).
-template <bool NT>
-__device__ __forceinline__ u32x4 load16(const uint16_t* p) {
-  if constexpr (NT) return __builtin_nontemporal_load((const u32x4*)p);
-  return *(const u32x4*)p;
-}
-template <bool NT, class V>
-__device__ __forceinline__ void store(void* p, V v) {
-  if constexpr (NT)
-    __builtin_nontemporal_store(v, (V*)p);
-  else
-    *(V*)p = v;
 }
 
 // Workgroups of WG threads, WG / TPR rows at a time.
@@ -140,28 +90,10 @@ __global__ __launch_bounds__(WG) void k_rmsnorm_quant(NormLaunch a) {
     if (a.y && in) store<false>(a.y + row * a.ldy + 8 * c, pack8<DT>(h[i]));
     if (!a.q) continue;
     // 16 neighbouring threads hold one block of 128 columns (those past K
-    // hold zeros); the bound keeps the scale of an all-zero block normal
-    amax = fmaxf(max16(amax), kF8Max * 0x1p-126f);
-    const float s = amax / kF8Max;
+    // hold zeros)
+    const float s = block_scale(max16(amax));
     if (in) {
-      // v / s by the product with 1 / s and one correction from the remainder.
-      // The product alone carries the reciprocal's rounding, which puts values
-      // on a border of two codes on either side of it.  (0.3 us of 78 at
-      // 16384 x 4096; the full division takes 2.3.)
-      const bool finite = s < __builtin_inff();
-      const float inv = 1.0f / s, den = finite ? s : 0.0f;  // v / inf: 0, without a remainder
-      float t[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        t[e] = h[i][e] * inv;
-        t[e] = __builtin_fmaf(__builtin_fmaf(-t[e], den, h[i][e]), inv, t[e]);
-      }
-      int lo = 0, hi = 0;
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], lo, false);
-      lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], hi, false);
-      hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], hi, true);
-      store<false>(a.q + row * a.ldq + 8 * c, u32x2{(uint32_t)lo, (uint32_t)hi});
+      store<false>(a.q + row * a.ldq + 8 * c, codes8(h[i], s));
       if (c % 16 == 0) a.scales[row * a.lds + c / 16] = s;
     }
   }

@@ -25,6 +25,7 @@
 
 #include "gmi_device.hpp"
 #include "gmi_internal.hpp"
+#include "gmi_rows.hpp"
 
 namespace gmi {
 
@@ -84,19 +85,6 @@ __device__ __forceinline__ uint32_t group_min(uint32_t v) {
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<L>(v, [](float a, float b) { return a + b; });
-}
-
-// e^d for d <= 0 (0 for -infinity, NaN for NaN) as 2^t with t = d log2 e rounded,
-// times e^(d - t ln 2), which is 1 + (d - t ln 2) to fp32.  2^t alone would carry
-// t's rounding, d 2^-24 of the result (3e-6 at d = -40).  (16384 tokens x 128:
-// routing 16.85 us, 16.65 without the factor and 17.2 with the library's expf;
-// backward 5.65, 5.4 and 5.8.)
-__device__ __forceinline__ float exp_le0(float d) {
-  constexpr float LOG2E = 1.44269504f, LN2 = 0.693147182f, LN2_REST = -1.90465434e-9f;
-  d = __builtin_elementwise_maximum(d, -104.0f);  // 2^-150, which is 0; an infinity would leave NaN below
-  const float t = d * LOG2E;
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, __builtin_fmaf(-LN2_REST, t, __builtin_fmaf(-LN2, t, d)), e);
 }
 
 // Order-preserving key of a logit: larger value, larger key; 0 for values that
@@ -366,6 +354,56 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouteLaunch a) {
   write_loss(a, ps, cnt, total, live_wg, wave_f);
 }
 
+// Column sums of the workgroups' 16-bit count matrix for expert tid: over all
+// workgroups and over those before b.  `part` is 2 x 8 RT_THREADS integers.
+__device__ __forceinline__ void sum_counts(const uint16_t* counts, int ld, int E, int wgs, int b,
+                                           int32_t (*part)[8 * RT_THREADS], int& st, int& sp) {
+  const int tid = threadIdx.x;
+  // a team of `team` threads (a power of two) reads one row of the matrix
+  int team = 1;
+  while (team < ld / 8) team *= 2;
+  const int slices = RT_THREADS / team, c = tid % team, sl = tid / team;
+  int tot[8], pre[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
+  if (c < ld / 8) {
+#pragma unroll 4
+    for (int q = sl; q < wgs; q += slices) {
+      const u32x4 v = *(const u32x4*)(counts + (int64_t)q * ld + 8 * c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = (int)(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xffffu);
+        tot[i] += n;
+        pre[i] += q < b ? n : 0;
+      }
+    }
+  }
+  // the teams of a wave, then the waves (or slices, of teams wider than a wave)
+  for (int d = team; d < 64; d *= 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      tot[i] += __shfl_xor(tot[i], d);
+      pre[i] += __shfl_xor(pre[i], d);
+    }
+  }
+  const int wide = max(team, 64), groups = RT_THREADS / wide;
+  if (tid % wide < team) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[0][(tid / wide) * team * 8 + c * 8 + i] = tot[i];
+      part[1][(tid / wide) * team * 8 + c * 8 + i] = pre[i];
+    }
+  }
+  __syncthreads();
+  st = sp = 0;
+  if (tid < E) {
+    for (int g = 0; g < groups; ++g) {
+      st += part[0][g * team * 8 + tid];
+      sp += part[1][g * team * 8 + tid];
+    }
+  }
+}
+
 // Second launch: every workgroup sums the count matrix for itself (totals, and
 // what lies before its own tokens), turns the ranks of its slots into rows and
 // writes both orders.  One further workgroup writes counts, offsets and loss;
@@ -399,49 +437,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int w
     }
     for (int q = tid; q < wgs; q += RT_THREADS) live += a.wg_live[q];
   }
-  // a team of `team` threads (a power of two) reads one row of the matrix
-  int team = 1;
-  while (team < ld / 8) team *= 2;
-  const int slices = RT_THREADS / team, c = tid % team, sl = tid / team;
-  int tot[8], pre[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
-  if (c < ld / 8) {
-#pragma unroll 4
-    for (int q = sl; q < wgs; q += slices) {
-      const u32x4 v = *(const u32x4*)(a.wg_counts + (int64_t)q * ld + 8 * c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int n = (int)(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xffffu);
-        tot[i] += n;
-        pre[i] += q < b ? n : 0;
-      }
-    }
-  }
-  // the teams of a wave, then the waves (or slices, of teams wider than a wave)
-  for (int d = team; d < 64; d *= 2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      tot[i] += __shfl_xor(tot[i], d);
-      pre[i] += __shfl_xor(pre[i], d);
-    }
-  }
-  const int wide = max(team, 64), groups = RT_THREADS / wide;
-  if (tid % wide < team) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      part[0][(tid / wide) * team * 8 + c * 8 + i] = tot[i];
-      part[1][(tid / wide) * team * 8 + c * 8 + i] = pre[i];
-    }
-  }
-  __syncthreads();
-  int st = 0, sp = 0;
-  if (tid < a.E) {
-    for (int g = 0; g < groups; ++g) {
-      st += part[0][g * team * 8 + tid];
-      sp += part[1][g * team * 8 + tid];
-    }
-  }
+  int st, sp;
+  sum_counts(a.wg_counts, ld, a.E, wgs, b, part, st, sp);
   int total;
   const int off = block_scan(st, wave_i, total);
   row0[tid] = off + sp;
@@ -479,6 +476,115 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int w
     if (s < s1) {
       x = a.indices[s];
       r = a.slot_row[s];
+    }
+  }
+}
+
+// Rows ordered by a number each carries.  A pass of a workgroup takes one row
+// per thread: the lanes of a wave that hold the same group find each other by
+// ballots over the number's bits, so a row's rank is a count of bits below its
+// lane, plus what earlier waves and passes put into the group.  Rows of no
+// group are a group of their own behind the others, whose counts go nowhere.
+// With one workgroup the places follow at once; otherwise the ranks wait in
+// `place` for k_group_place.
+__global__ __launch_bounds__(RT_THREADS) void k_group(GroupLaunch a) {
+  __shared__ uint16_t hist[RT_THREADS / 64][kMaxGroups + 8];
+  __shared__ int base[kMaxGroups + 8];
+  __shared__ int wave_i[RT_THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int first = blockIdx.x * a.rows_per_wg, end = min(a.n, first + a.rows_per_wg);
+  for (int g = tid; g <= a.G; g += RT_THREADS) {
+    base[g] = 0;
+    for (int w = 0; w < RT_THREADS / 64; ++w) hist[w][g] = 0;
+  }
+  __syncthreads();
+  for (int s0 = first; s0 < end; s0 += RT_THREADS) {
+    const int s = s0 + tid;
+    const bool in = s < end;
+    int g = in ? a.index[s] : 0;
+    if ((uint32_t)g >= (uint32_t)a.G) g = a.G;
+    uint64_t same = __ballot(in);
+    for (int bit = 0; 1 << bit <= a.G; ++bit) {
+      const uint64_t set = __ballot(g >> bit & 1);
+      same &= g >> bit & 1 ? set : ~set;
+    }
+    const int before = __popcll(same & ((1ull << lane) - 1ull));
+    if (in && before == 0) hist[wave][g] = (uint16_t)__popcll(same);
+    __syncthreads();
+    if (in) {
+      int r = base[g] + before;
+      for (int w = 0; w < wave; ++w) r += hist[w][g];
+      a.place[s] = r;
+    }
+    __syncthreads();
+    for (int q = tid; q <= a.G; q += RT_THREADS) {
+      int c = base[q];
+      for (int w = 0; w < RT_THREADS / 64; ++w) {
+        c += hist[w][q];
+        hist[w][q] = 0;
+      }
+      base[q] = c;
+    }
+    __syncthreads();
+  }
+  if (gridDim.x > 1) {
+    const int ld = route_ld(a.G);
+    if (tid < ld) a.wg_counts[(int64_t)blockIdx.x * ld + tid] = tid < a.G ? (uint16_t)base[tid] : 0;
+    return;
+  }
+  int total;
+  const int off = block_scan(tid < a.G ? base[tid] : 0, wave_i, total);
+  if (tid < a.G) {
+    a.offsets[tid] = off;
+    base[tid] = off;
+  }
+  if (tid == 0) {
+    a.offsets[a.G] = total;
+    base[a.G] = total;
+  }
+  __syncthreads();
+  for (int s = tid; s < a.n; s += RT_THREADS) {
+    int g = a.index[s];
+    if ((uint32_t)g >= (uint32_t)a.G) g = a.G;
+    const int r = base[g] + a.place[s];  // this thread's own rank
+    a.order[r] = s;
+    a.place[s] = g < a.G ? r : -1;
+  }
+}
+
+__global__ __launch_bounds__(RT_THREADS) void k_group_place(GroupLaunch a, int wgs) {
+  __shared__ int32_t part[2][8 * RT_THREADS];
+  __shared__ int row0[kMaxGroups + 1];
+  __shared__ int wave_i[RT_THREADS / 64];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int first = b * a.rows_per_wg, end = min(a.n, first + a.rows_per_wg);
+  int s = first + tid;
+  int g = 0, r = 0;
+  if (s < end) {
+    g = a.index[s];
+    r = a.place[s];
+  }
+  int st, sp;
+  sum_counts(a.wg_counts, route_ld(a.G), a.G, wgs, b, part, st, sp);
+  int total, before;
+  const int off = block_scan(st, wave_i, total);
+  block_scan(sp, wave_i, before);
+  if (tid < a.G) row0[tid] = off + sp;
+  if (tid == 0) row0[a.G] = total + first - before;  // rows of no group before this workgroup
+  if (b == 0) {
+    if (tid < a.G) a.offsets[tid] = off;
+    if (tid == 0) a.offsets[a.G] = total;
+  }
+  __syncthreads();
+  while (s < end) {
+    if ((uint32_t)g >= (uint32_t)a.G) g = a.G;
+    r += row0[g];
+    a.order[r] = s;
+    a.place[s] = g < a.G ? r : -1;
+    s += RT_THREADS;
+    if (s < end) {
+      g = a.index[s];
+      r = a.place[s];
     }
   }
 }
@@ -625,6 +731,30 @@ hipError_t launch_route_bwd(const RouteBwdLaunch& a, int dtype, hipStream_t stre
   const int64_t need = ((int64_t)a.T + groups - 1) / groups, most = 4 * (int64_t)device_cu_count();
   const unsigned grid = (unsigned)(need < most ? need : most);
   GMI_ROUTE(k_route_bwd, dtype, a.E, grid, 256, stream, a);
+  return hipGetLastError();
+}
+
+GroupPlan plan_group(int n, int G) {
+  GroupPlan p;
+  // one launch up to four passes of a workgroup; then 256 workgroups, whose counts have 16 bits
+  const int64_t passes = ((int64_t)n + RT_THREADS - 1) / RT_THREADS;
+  const int64_t per = passes <= 4 ? std::max<int64_t>(passes, 1)
+                                  : std::min<int64_t>((passes + 255) / 256, 65535 / RT_THREADS);
+  p.rows_per_wg = (int)(per * RT_THREADS);
+  p.wgs = (int)std::max<int64_t>((passes + per - 1) / per, 1);
+  p.bytes = p.wgs > 1 ? (size_t)p.wgs * ((G + 7) / 8 * 8) * 2 : 0;
+  return p;
+}
+
+hipError_t launch_group(const GroupLaunch& args, void* workspace, hipStream_t stream) {
+  GroupLaunch a = args;
+  const GroupPlan p = plan_group(a.n, a.G);
+  a.rows_per_wg = p.rows_per_wg;
+  a.wg_counts = (uint16_t*)workspace;
+  hipLaunchKernelGGL(k_group, dim3(p.wgs), dim3(RT_THREADS), 0, stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.wgs == 1) return e;
+  hipLaunchKernelGGL(k_group_place, dim3(p.wgs), dim3(RT_THREADS), 0, stream, a, p.wgs);
   return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
-// py_calls.cpp -- argument marshalling of the block-scaled fp8
-// mixture-of-experts calls for Python.
+// py_calls.cpp -- argument marshalling for Python of the mixture-of-experts
+// calls and of the adapters' product.
 //
 // A call on a few tokens takes the device 3 to 6 us; reading types, shapes,
 // strides and addresses of up to nine tensors attribute by attribute and
@@ -25,6 +25,13 @@ decltype(&gmi_gemm_f8_block) f_gemm_f8_block;
 decltype(&gmi_gemm_f8_block_grouped) f_gemm_f8_block_grouped;
 decltype(&gmi_moe_route) f_moe_route;
 decltype(&gmi_moe_route_bwd) f_moe_route_bwd;
+decltype(&gmi_group_rows) f_group_rows;
+decltype(&gmi_moe_permute) f_moe_permute;
+decltype(&gmi_moe_unpermute) f_moe_unpermute;
+decltype(&gmi_moe_unpermute_bwd) f_moe_unpermute_bwd;
+decltype(&gmi_swiglu_quant) f_swiglu_quant;
+decltype(&gmi_swiglu_bwd) f_swiglu_bwd;
+decltype(&gmi_gemm_lora) f_gemm_lora;
 
 // a refusal: becomes ValueError
 struct Refused : std::runtime_error {
@@ -319,6 +326,243 @@ PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The calls below also hold their tensors to one device and ask Python for a
+// stream of that device (stream_on), so that no kernel runs beside its memory.
+PyObject* stream_on;
+struct Place {
+  int device = -1;
+  void add(const at::Tensor& t, const char* name) {
+    if (!t.is_cuda()) refuse("%s must be on the device", name);
+    if (device < 0) device = t.get_device();
+    if (device != t.get_device()) refuse("%s is on another device than the other tensors", name);
+  }
+  Matrix matrix(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+    const Matrix m = ::matrix(o, name, rows, cols, type);
+    add(tensor(o, name), name);
+    return m;
+  }
+  Matrix matrix_or_none(PyObject* o, const char* name, int64_t rows, int64_t cols, at::ScalarType type) {
+    return o == Py_None ? Matrix{} : matrix(o, name, rows, cols, type);
+  }
+  template <class T>
+  T* vector(PyObject* o, const char* name, int64_t n, at::ScalarType type) {
+    if (o == Py_None) return nullptr;
+    void* p = ::vector(o, name, n, type);
+    add(tensor(o, name), name);
+    return (T*)p;
+  }
+  template <class T>
+  T* vector_needed(PyObject* o, const char* name, int64_t n, at::ScalarType type) {
+    tensor(o, name);
+    return vector<T>(o, name, n, type);
+  }
+  Scratch scratch(PyObject* o) {
+    const Scratch s = ::scratch(o);
+    if (s.p || s.bytes) add(tensor(o, "workspace"), "workspace");
+    return s;
+  }
+  void* stream(PyObject* o) {
+    PyObject* d = PyLong_FromLong(device);
+    if (!d) throw PythonError{};
+    PyObject* v = PyObject_CallFunctionObjArgs(stream_on, o, d, nullptr);
+    Py_DECREF(d);
+    if (!v) throw PythonError{};
+    void* p = PyLong_AsVoidPtr(v);
+    Py_DECREF(v);
+    if (!p && PyErr_Occurred()) throw PythonError{};
+    return p;
+  }
+};
+
+// index, groups, offsets, order, place, workspace, stream
+PyObject* group_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("group_rows", n, 7, (void*)f_group_rows, [&] {
+    Place at;
+    const int64_t rows = tensor(a[0], "index").numel(), groups = integer(a[1]);
+    const int32_t* index = at.vector_needed<int32_t>(a[0], "index", rows, I32);
+    if (groups < 1 || groups > INT32_MAX - 1) refuse("groups must be positive");
+    int32_t* offsets = at.vector_needed<int32_t>(a[2], "offsets", groups + 1, I32);
+    int32_t* order = at.vector_needed<int32_t>(a[3], "order", rows, I32);
+    int32_t* place = at.vector_needed<int32_t>(a[4], "place", rows, I32);
+    const Scratch ws = at.scratch(a[5]);
+    const int32_t n32 = size32(rows, "rows");
+    void* st = at.stream(a[6]);
+    return without_gil(
+        [&] { return f_group_rows(n32, (int32_t)groups, index, offsets, order, place, ws.p, ws.bytes, st); });
+  });
+}
+
+// slot_row [tokens][k]: address and sizes
+struct Slots {
+  const int32_t* p;
+  int64_t T, k;
+};
+Slots slots_of(Place& at, PyObject* o) {
+  const at::Tensor& t = tensor(o, "slot_row");
+  if (t.dim() != 2) refuse("slot_row must be [tokens][k]");
+  const int64_t T = t.size(0), k = t.size(1);
+  return {at.vector_needed<int32_t>(o, "slot_row", T * k, I32), T, k};
+}
+// a row operand that fixes type, rows and columns
+struct Rows {
+  Matrix m;
+  int64_t rows, cols;
+  at::ScalarType type;
+  gmi_dtype dt;
+};
+Rows rows_of(Place& at, PyObject* o, const char* name, bool f8 = false) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() != 2) refuse("%s must have two dimensions", name);
+  const at::ScalarType type = t.scalar_type();
+  const gmi_dtype dt = f8 && type == F8 ? GMI_F8E4M3 : half_type(type, name);
+  const int64_t rows = t.size(0), cols = t.size(1);
+  return {at.matrix(o, name, rows, cols, type), rows, cols, type, dt};
+}
+
+// x, slot_row, x_scales, out, out_scales, stream
+PyObject* moe_permute(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("moe_permute", n, 6, (void*)f_moe_permute, [&] {
+    Place at;
+    const Rows x = rows_of(at, a[0], "x", true);
+    const Slots s = slots_of(at, a[1]);
+    if (s.T != x.rows) refuse("x and slot_row disagree on the tokens");
+    const at::Tensor& ot = tensor(a[3], "out");
+    const int64_t rows = ot.dim() ? ot.size(0) : 0, nb = blocks(x.cols);
+    const Matrix out = at.matrix(a[3], "out", rows, x.cols, x.type),
+                 xs = at.matrix_or_none(a[2], "scales", x.rows, nb, F32),
+                 os = at.matrix_or_none(a[4], "out_scales", rows, nb, F32);
+    const int32_t t32 = size32(s.T, "tokens"), k32 = size32(s.k, "k"), c32 = size32(x.cols, "K"),
+                  r32 = size32(rows, "rows");
+    void* st = at.stream(a[5]);
+    return without_gil([&] {
+      return f_moe_permute(t32, k32, c32, x.dt, x.m.p, x.m.ld, (const float*)xs.p, xs.ld, s.p, r32, out.p, out.ld,
+                           (float*)os.p, os.ld, st);
+    });
+  });
+}
+
+// y, slot_row, weights, add, out, stream
+PyObject* moe_unpermute(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("moe_unpermute", n, 6, (void*)f_moe_unpermute, [&] {
+    Place at;
+    const Rows y = rows_of(at, a[0], "rows");
+    const Slots s = slots_of(at, a[1]);
+    const float* w = at.vector<float>(a[2], "weights", s.T * s.k, F32);
+    const Matrix add = at.matrix_or_none(a[3], "add", s.T, y.cols, y.type),
+                 out = at.matrix(a[4], "out", s.T, y.cols, y.type);
+    const int32_t t32 = size32(s.T, "tokens"), k32 = size32(s.k, "k"), c32 = size32(y.cols, "K"),
+                  r32 = size32(y.rows, "rows");
+    void* st = at.stream(a[5]);
+    return without_gil([&] {
+      return f_moe_unpermute(t32, k32, c32, y.dt, y.m.p, y.m.ld, r32, s.p, w, add.p, add.ld, out.p, out.ld, st);
+    });
+  });
+}
+
+// dout, slot_row, weights, y, drows, q, scales, dweights, stream
+PyObject* moe_unpermute_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("moe_unpermute_bwd", n, 9, (void*)f_moe_unpermute_bwd, [&] {
+    Place at;
+    const Rows d = rows_of(at, a[0], "dout");
+    const Slots s = slots_of(at, a[1]);
+    if (s.T != d.rows) refuse("dout and slot_row disagree on the tokens");
+    const float* w = at.vector<float>(a[2], "weights", s.T * s.k, F32);
+    PyObject* first = a[4] != Py_None ? a[4] : a[5];
+    const at::Tensor& ft = tensor(first, "drows or q");
+    const int64_t rows = ft.dim() ? ft.size(0) : 0;
+    const Matrix y = at.matrix_or_none(a[3], "rows", rows, d.cols, d.type),
+                 dr = at.matrix_or_none(a[4], "drows", rows, d.cols, d.type),
+                 q = at.matrix_or_none(a[5], "q", rows, d.cols, F8),
+                 sc = at.matrix_or_none(a[6], "scales", rows, blocks(d.cols), F32);
+    float* dw = at.vector<float>(a[7], "dweights", s.T * s.k, F32);
+    const int32_t t32 = size32(s.T, "tokens"), k32 = size32(s.k, "k"), c32 = size32(d.cols, "K"),
+                  r32 = size32(rows, "rows");
+    void* st = at.stream(a[8]);
+    return without_gil([&] {
+      return f_moe_unpermute_bwd(t32, k32, c32, d.dt, d.m.p, d.m.ld, s.p, w, y.p, y.ld, r32, dr.p, dr.ld, q.p, q.ld,
+                                 (float*)sc.p, sc.ld, dw, st);
+    });
+  });
+}
+
+// gate and up side by side: rows and the columns of each
+struct Gated {
+  Rows a;
+  int32_t rows, N;
+};
+Gated gated_of(Place& at, PyObject* o) {
+  const Rows r = rows_of(at, o, "a");
+  if (r.cols % 2) refuse("a must hold gate and up side by side");
+  return {r, size32(r.rows, "rows"), size32(r.cols / 2, "N")};
+}
+
+// a, live, y, q, scales, stream
+PyObject* swiglu_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("swiglu_quant", n, 6, (void*)f_swiglu_quant, [&] {
+    Place at;
+    const Gated g = gated_of(at, a[0]);
+    const int32_t* live = at.vector<int32_t>(a[1], "live", 1, I32);
+    const Matrix y = at.matrix_or_none(a[2], "y", g.rows, g.N, g.a.type),
+                 q = at.matrix_or_none(a[3], "q", g.rows, g.N, F8),
+                 s = at.matrix_or_none(a[4], "scales", g.rows, blocks(g.N), F32);
+    void* st = at.stream(a[5]);
+    return without_gil([&] {
+      return f_swiglu_quant(g.rows, g.N, g.a.dt, g.a.m.p, g.a.m.ld, live, y.p, y.ld, q.p, q.ld, (float*)s.p, s.ld, st);
+    });
+  });
+}
+
+// dact, a, live, da, q, scales, stream
+PyObject* swiglu_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("swiglu_bwd", n, 7, (void*)f_swiglu_bwd, [&] {
+    Place at;
+    const Gated g = gated_of(at, a[1]);
+    const Matrix d = at.matrix(a[0], "dact", g.rows, g.N, g.a.type);
+    const int32_t* live = at.vector<int32_t>(a[2], "live", 1, I32);
+    const int64_t cols = 2 * (int64_t)g.N;
+    const Matrix da = at.matrix_or_none(a[3], "da", g.rows, cols, g.a.type),
+                 q = at.matrix_or_none(a[4], "q", g.rows, cols, F8),
+                 s = at.matrix_or_none(a[5], "scales", g.rows, blocks(cols), F32);
+    void* st = at.stream(a[6]);
+    return without_gil([&] {
+      return f_swiglu_bwd(g.rows, g.N, g.a.dt, d.p, d.ld, g.a.m.p, g.a.m.ld, live, da.p, da.ld, q.p, q.ld, (float*)s.p,
+                          s.ld, st);
+    });
+  });
+}
+
+// X, A, B, index, scales, order, base, Y, workspace, stream
+PyObject* gemm_lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("gemm_lora", n, 10, (void*)f_gemm_lora, [&] {
+    Place at;
+    const Rows x = rows_of(at, a[0], "X");
+    const at::Tensor &A = tensor(a[1], "A"), &B = tensor(a[2], "B");
+    if (A.dim() != 3 || B.dim() != 3 || A.scalar_type() != x.type || B.scalar_type() != x.type || A.size(2) != x.cols ||
+        B.size(0) != A.size(0) || B.size(2) != A.size(1))
+      refuse("A must be [adapters][rank][K] and B [adapters][N][rank], of X's type");
+    at.add(A, "A");
+    at.add(B, "B");
+    const int64_t L = A.size(0), rank = A.size(1), N = B.size(1), M = x.rows, K = x.cols;
+    if ((K > 1 && A.stride(2) != 1) || (rank > 1 && B.stride(2) != 1))
+      refuse("A and B must have unit stride along their rows");
+    const int32_t* index = at.vector_needed<int32_t>(a[3], "index", M, I32);
+    const float* scales = at.vector<float>(a[4], "scales", L, F32);
+    const int32_t* order = at.vector<int32_t>(a[5], "order", M, I32);
+    const Matrix base = at.matrix_or_none(a[6], "base", M, N, x.type), y = at.matrix(a[7], "Y", M, N, x.type);
+    const Scratch ws = at.scratch(a[8]);
+    const int32_t m32 = size32(M, "M"), n32 = size32(N, "N"), k32 = size32(K, "K"), r32 = size32(rank, "rank"),
+                  l32 = size32(L, "adapters");
+    const int64_t lda = leading(rank, K, A.stride(1)), ldb = leading(N, rank, B.stride(1));
+    const int64_t as = A.stride(0), bs = B.stride(0);
+    const void *ap = A.data_ptr(), *bp = B.data_ptr();
+    void* st = at.stream(a[9]);
+    return without_gil([&] {
+      return f_gemm_lora(m32, n32, k32, r32, l32, x.dt, x.m.p, x.m.ld, ap, lda, as, bp, ldb, bs, scales, index, order,
+                         base.p, base.ld, y.p, y.ld, ws.p, ws.bytes, st);
+    });
+  });
+}
+
 // addresses of the library's functions, in the order of the declarations above,
 // and the function that turns a stream argument into a handle
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -343,10 +587,38 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// the same for the calls that hold their tensors to one device; the function
+// takes a stream argument and a device number
+PyObject* bind_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) return PyErr_Format(PyExc_TypeError, "bind_rows takes 7 addresses and a function, got %zd arguments", n);
+  void* p[7];
+  for (int i = 0; i < 7; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (!p[i]) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_rows: a NULL address");
+      return nullptr;
+    }
+  }
+  Py_INCREF(a[7]);
+  Py_XDECREF(stream_on);
+  stream_on = a[7];
+  f_group_rows = (decltype(f_group_rows))p[0];
+  f_moe_permute = (decltype(f_moe_permute))p[1];
+  f_moe_unpermute = (decltype(f_moe_unpermute))p[2];
+  f_moe_unpermute_bwd = (decltype(f_moe_unpermute_bwd))p[3];
+  f_swiglu_quant = (decltype(f_swiglu_quant))p[4];
+  f_swiglu_bwd = (decltype(f_swiglu_bwd))p[5];
+  f_gemm_lora = (decltype(f_gemm_lora))p[6];
+  Py_RETURN_NONE;
+}
+
 #define GMI_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GMI_METHOD(bind),          GMI_METHOD(rmsnorm_quant),         GMI_METHOD(rmsnorm_bwd),
                          GMI_METHOD(gemm_f8_block), GMI_METHOD(gemm_f8_block_grouped), GMI_METHOD(moe_route),
-                         GMI_METHOD(moe_route_bwd), {nullptr, nullptr, 0, nullptr}};
+                         GMI_METHOD(moe_route_bwd), GMI_METHOD(bind_rows),             GMI_METHOD(group_rows),
+                         GMI_METHOD(moe_permute),   GMI_METHOD(moe_unpermute),         GMI_METHOD(moe_unpermute_bwd),
+                         GMI_METHOD(swiglu_quant),  GMI_METHOD(swiglu_bwd),            GMI_METHOD(gemm_lora),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Argument marshalling of libgmi.so's newer calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

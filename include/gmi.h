@@ -550,6 +550,133 @@ gmi_status gmi_moe_route_bwd(int32_t tokens, int32_t experts, int32_t k, const v
                              const float* weights, const int32_t* offsets, const int32_t* live,
                              const float* dweights, const float* dloss, void* dlogits, int64_t ldd, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rows between the products of a mixture-of-experts layer.  A slot is one of
+ * a token's k experts; slot_row[tokens][k] (gmi_moe_route, or `place` of
+ * gmi_group_rows) is the row that a slot has among the experts' rows.  A row
+ * number outside [0, rows) is a slot without an expert: nothing is read or
+ * written for it.  No two slots may share a row.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of the workspace gmi_group_rows needs (0 for up to 4096 rows). */
+size_t gmi_group_rows_workspace_bytes(int32_t n, int32_t groups);
+
+/* Rows ordered by a number that each carries (its expert, its adapter), for
+ * routers of the caller's own and for gmi_gemm_lora:
+ *   offsets[g], offsets[groups]  rows of the groups before g, of all groups
+ *   order[r]  the row at place r: sorted by group, inside a group by row; rows
+ *             of no group (index outside [0, groups)) come last, in order
+ *   place[i]  the place of row i; -1 for rows of no group.
+ * With the experts of the slots as index, offsets, order and place serve as
+ * offsets, row_slot and slot_row of gmi_moe_route (whose row_slot holds -1
+ * where order goes on with the slots of no expert).
+ *   n         >= 0, below 2^31 - 2^17; groups 1 .. 1024.
+ *   index, order, place  int32 [n], none overlapping; offsets int32 [groups + 1].
+ *   workspace gmi_group_rows_workspace_bytes(n, groups) bytes, 16-byte
+ *             aligned; may be NULL when that is 0. */
+gmi_status gmi_group_rows(int32_t n, int32_t groups, const int32_t* index, int32_t* offsets, int32_t* order,
+                          int32_t* place, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Every token's row copied to the rows of its slots: out[slot_row[t][i]] =
+ * x[t], bit for bit, and its scales with it.  Its gradient is
+ * gmi_moe_unpermute without weights.
+ *   dtype      GMI_F8E4M3 (K, ldx, ldo multiples of 16), GMI_F16 or GMI_BF16.
+ *   x_scales, out_scales  fp32 [tokens][ldxs], [rows][ldos], ceil(K / 128) a
+ *              row; both or neither, with fp8 only.
+ *   tokens * k < 2^31 - 2^17; k 1 .. 16.
+ * Rows of out that no slot has are not written. */
+gmi_status gmi_moe_permute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* x, int64_t ldx,
+                           const float* x_scales, int64_t ldxs, const int32_t* slot_row, int32_t rows, void* out,
+                           int64_t ldo, float* out_scales, int64_t ldos, void* stream);
+
+/* The experts' rows back to the tokens:
+ *   out[t] = RN(sum_i weights[t][i] * y[slot_row[t][i]] + add[t])
+ * fp32, summed in the order of i.  A slot without a row adds nothing, whatever
+ * its weight.
+ *   y        [rows][ldy]; out [tokens][ldo]; `dtype` (GMI_F16 or GMI_BF16).
+ *   weights  fp32 [tokens][k], or NULL for 1.
+ *   add      [tokens][ldadd] (a shared expert, the residual stream) or NULL;
+ *            out may be add exactly.
+ * K a multiple of 8; other sizes as for gmi_moe_permute. */
+gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* y, int64_t ldy,
+                             int32_t rows, const int32_t* slot_row, const float* weights, const void* add,
+                             int64_t ldadd, void* out, int64_t ldo, void* stream);
+
+/* Gradients of gmi_moe_unpermute (that of `add` is dout itself):
+ *   g = weights[t][i] * dout[t]          (fp32) for row slot_row[t][i]
+ *   drows = RN(g), or q = e4m3(g / s) with s = max(max |g| over the 128-column
+ *   block, 448 * 2^-126) / 448, the fp8 operand of the data gradient's product
+ *   dweights[t][i] = sum over columns of dout[t] * y[slot_row[t][i]]   (fp32; 0
+ *   for a slot without a row)
+ *   dout       [tokens][lddout], `dtype`.
+ *   y          as the forward read it; needed with dweights only.
+ *   drows      [rows][lddrows], `dtype`; or NULL, and q fp8 [rows][ldq] (8-byte
+ *              aligned, ldq a multiple of 8, of 16 where a GEMM call reads it)
+ *              with scales fp32 [rows][lds].  drows may be y exactly.
+ *   dweights   fp32 [tokens][k] or NULL (a frozen router).
+ * A NaN among g stands in q and does not enter the block's maximum.  Rows that
+ * no slot has are not written.  Sizes as for gmi_moe_unpermute. */
+gmi_status gmi_moe_unpermute_bwd(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* dout,
+                                 int64_t lddout, const int32_t* slot_row, const float* weights, const void* y,
+                                 int64_t ldy, int32_t rows, void* drows, int64_t lddrows, void* q, int64_t ldq,
+                                 float* scales, int64_t lds, float* dweights, void* stream);
+
+/* Gated activation of the two halves of a row, for the next product:
+ *   v = g / (1 + e^-g) * u,  g = a[r][0 .. N - 1], u = a[r][N .. 2 N - 1]   (fp32)
+ *   y = RN(v); q = e4m3(v / s), s as for gmi_rmsnorm_quant.
+ *   a      [rows][lda], lda >= 2 N, dtype GMI_F16 or GMI_BF16; N a multiple of
+ *          8, at most 2^22.
+ *   live   one int32 on the device: only rows below it are read and written
+ *          (offsets[E] of the routing); NULL: all.
+ *   y      [rows][ldy], `dtype`; q fp8 [rows][ldq] (8-byte aligned, ldq a
+ *          multiple of 8) with scales fp32 [rows][lds].  One of both at least. */
+gmi_status gmi_swiglu_quant(int32_t rows, int32_t N, gmi_dtype dtype, const void* a, int64_t lda, const int32_t* live,
+                            void* y, int64_t ldy, void* q, int64_t ldq, float* scales, int64_t lds, void* stream);
+
+/* Gradient of gmi_swiglu_quant's v, gate and up side by side, with
+ * sg = 1 / (1 + e^-g):
+ *   dg = dact u sg (1 + g (1 - sg)),   du = dact g sg      (fp32)
+ *   da = RN([dg | du]), or q and scales of [dg | du] as one row of 2 N columns
+ *        (a block of 128 may hold the end of dg and the start of du).
+ *   dact   [rows][lddact], `dtype`.
+ *   da     [rows][ldda], `dtype`; or NULL, and q fp8 [rows][ldq] with scales
+ *          fp32 [rows][lds], lds >= ceil(2 N / 128).  da may be a exactly.
+ * Other arguments as for gmi_swiglu_quant. */
+gmi_status gmi_swiglu_bwd(int32_t rows, int32_t N, gmi_dtype dtype, const void* dact, int64_t lddact, const void* a,
+                          int64_t lda, const int32_t* live, void* da, int64_t ldda, void* q, int64_t ldq, float* scales,
+                          int64_t lds, void* stream);
+
+/* Bytes of the workspace gmi_gemm_lora needs for this shape: fp32 sums of
+ * X A^T over runs of K. */
+size_t gmi_gemm_lora_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t rank);
+
+/* Low-rank adapters of many requests beside one dense product:
+ *   Y[m] = RN(base[m] + scales[a] * (X[m] A_a^T) B_a^T),  a = index[m]
+ * with A_a = A + a * a_stride [rank][lda] and B_a = B + a * b_stride [N][ldb].
+ * Sums are fp32; X A^T enters the second product as two terms of the type,
+ * together good to 2^-17 (bf16) or 2^-22 (fp16) of a row's largest.  A row
+ * whose index lies outside [0, adapters) gets base (zeros without one).
+ *   X, base, Y  [M][ldx], [M][ldbase], [M][ldy]; A, B: dtype GMI_F16 or GMI_BF16.
+ *   N, K, rank  multiples of 8; rank 1 .. 128 (pad smaller adapters with
+ *            zeros); M at most 2^29.
+ *   scales   fp32 [adapters] or NULL for 1.
+ *   index    int32 [M].
+ *   order    int32 [M], the rows in an order that brings those of one adapter
+ *            together (order of gmi_group_rows over index), each row once: what
+ *            takes the time is the number of runs of one adapter among every 64
+ *            rows of it.  NULL: rows as they come, the same results.  An entry
+ *            outside [0, M) is skipped; rows that order leaves out are not written.
+ *   base     the dense product's result, or NULL; Y may be base exactly (same
+ *            pointer and leading dimension).
+ *   a_stride, b_stride  at least one adapter's data when adapters > 1, multiples of 8.
+ *   workspace gmi_gemm_lora_workspace_bytes(M, N, K, rank) bytes, 16-byte
+ *            aligned, scratch. */
+gmi_status gmi_gemm_lora(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t adapters, gmi_dtype dtype,
+                         const void* X, int64_t ldx, const void* A, int64_t lda, int64_t a_stride, const void* B,
+                         int64_t ldb, int64_t b_stride, const float* scales, const int32_t* index,
+                         const int32_t* order, const void* base, int64_t ldbase, void* Y, int64_t ldy,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Text of the last failed check or HIP error on the calling thread ("" if
  * none).  The pointer stays valid until the next gmi_* call on that thread. */
 const char* gmi_last_error(void);
