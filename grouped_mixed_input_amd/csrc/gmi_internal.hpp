@@ -317,6 +317,7 @@ struct SwigluLaunch {
   uint8_t* q;
   float* scales;
   int64_t lda, ldd, ldy, ldq, lds;
+  uint32_t magic, magic_shift;  // the launch's division by the blocks of a row
 };
 hipError_t launch_swiglu(const SwigluLaunch& a, int dtype, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const SwigluLaunch& a, int dtype, hipStream_t stream);

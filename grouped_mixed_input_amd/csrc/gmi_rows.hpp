@@ -46,7 +46,7 @@ constexpr float kF8Max = 448.0f;
 
 // One 16-byte access, or past the caches (NT).
 template <bool NT>
-__device__ __forceinline__ u32x4 load16(const uint16_t* p) {
+__device__ __forceinline__ u32x4 load16(const void* p) {
   if constexpr (NT) return __builtin_nontemporal_load((const u32x4*)p);
   return *(const u32x4*)p;
 }
