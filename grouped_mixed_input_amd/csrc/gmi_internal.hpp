@@ -330,7 +330,7 @@ struct LoraLaunch {
   const int32_t *index, *order;  // order NULL: rows as they come
   uint16_t* Y;
   int64_t ldx, lda, a_stride, ldb, b_stride, ldbase, ldy;
-  float* part;  // [splits][M][rank]: X A^T over runs of K, rows in the order of the call
+  float* part;  // [splits][rank / 4][M][4]: X A^T over runs of K, rows in the order of the call
   int splits;
 };
 constexpr int kMaxLoraRank = 128;

@@ -47,7 +47,9 @@ def up(*tensors):
     (1, 8, 8, 8, 1, 1), (1, 512, 512, 16, 3, 1), (2, 64, 40, 8, 2, 1), (16, 1032, 2056, 16, 16, 1),
     (17, 264, 328, 24, 5, 1), (64, 256, 1024, 32, 64, 1), (65, 200, 264, 40, 4, 7), (100, 72, 520, 64, 3, 33),
     (128, 520, 256, 72, 2, 64), (200, 136, 300 // 8 * 8, 128, 3, 20), (333, 2000, 2056, 40, 12, 7),
-    (1000, 256, 768, 16, 300, 1), (700, 128, 4096, 48, 2, 350)])
+    (1000, 256, 768, 16, 300, 1), (700, 128, 4096, 48, 2, 350), (511, 264, 1032, 64, 6, 40),
+    (512, 72, 40, 8, 3, 100), (513, 8, 8, 64, 5, 9), (900, 200, 2056, 72, 4, 130), (1500, 1032, 264, 128, 3, 200),
+    (640, 136, 1000, 32, 700, 1), (2048, 520, 4096, 24, 8, 300), (777, 328, 648, 96, 2, 64)])
 def test_lora(gmi, dtype, M, N, K, rank, adapters, run):
     X, A, B, index, scales, base = case(M, N, K, rank, adapters, dtype, run=run)
     d = up(X, A, B, index, scales, base)
