@@ -1,8 +1,8 @@
 """One mixture-of-experts layer over block-scaled fp8 operands, as a program runs it.
 
   forward   residual add + RMS norm -> fp8 rows with scales; router -> experts, weights, row order, balance loss;
-            rows gathered by expert; up and gate projection per expert; SiLU; down projection per expert;
-            weighted sum of each token's experts
+            rows to their experts; up and gate projection per expert; gated activation in fp8; down projection per
+            expert; weighted sum of each token's experts
   backward  of the routing weights, the balance loss and the norm, and with through_experts of the experts' input, the
             layer's whole data gradient: the same grouped products with the transposed weights, on gradients that are
             quantised as activations are (the experts' weights are frozen)
@@ -63,47 +63,39 @@ class Layer:
         self.down = quantize_weight(randn(experts, hidden, inner, std=inner ** -0.5))
         self.up_t, self.down_t = transposed(*self.up), transposed(*self.down)
 
-    def forward(self, x, residual, mask=None):
-        """Returns the layer's output, the new residual stream and what the backward pass needs."""
+    def forward(self, x, residual, mask=None, per_slot=True):
+        """Returns the layer's output, the new residual stream and what the backward pass needs; with it, for
+        inspection, the experts' output of each slot in float32 (None without per_slot)."""
         h, y = torch.empty_like(x), torch.empty_like(x)
         q, s = gmi.rmsnorm_quant(x, self.norm, residual=residual, h=h, y=y)
         logits = y @ self.router.t()
         r = gmi.moe_route(logits, self.top, mask=mask)
-        # rows past the last routed one hold -1: they belong to no expert, any token will do
-        token = torch.div(r.row_slot, self.top, rounding_mode="floor").clamp_min(0).long()
-        a = gmi.gemm_f8_block_grouped(r.offsets, q.view(torch.uint8)[token].view(F8), s[token], *self.up)
-        routed = torch.arange(len(token), device=x.device) < r.offsets[-1]
-        act = torch.nn.functional.silu(a[:, : self.inner].float()) * a[:, self.inner:].float()
-        aq, a_scales = quantize(torch.where(routed[:, None], act, 0.0))
-        d = gmi.gemm_f8_block_grouped(r.offsets, aq, a_scales, *self.down)
-        expert_out = torch.where(r.slot_row[..., None] >= 0, d[r.slot_row.clamp_min(0).long()].float(), 0.0)
-        out = (expert_out * r.weights[..., None]).sum(1).to(x.dtype)
-        return out, h, (h, y, logits, r, expert_out, (mask, token, routed, a))
+        # rows past the last routed one belong to no expert: nothing reads or writes them
+        a = gmi.gemm_f8_block_grouped(r.offsets, *gmi.moe_permute(q, r.slot_row, scales=s), *self.up)
+        d = gmi.gemm_f8_block_grouped(r.offsets, *gmi.swiglu_quant(a, live=r.offsets[-1:]), *self.down)
+        out = gmi.moe_unpermute(d, r.slot_row, weights=r.weights)
+        expert_out = None
+        if per_slot:
+            expert_out = torch.where(r.slot_row[..., None] >= 0, d[r.slot_row.clamp_min(0).long()].float(), 0.0)
+        return out, h, (h, y, logits, r, expert_out, (mask, a, d))
 
     def backward(self, dout, dloss, saved, dh_out=None, through_experts=False):
         """Gradients of the sum before the norm (through the routing weights and the balance loss, past the norm:
         dh_out, and through the experts if asked), of the norm's and of the router's weight."""
-        h, y, logits, r, expert_out, rows = saved
-        dweights = (expert_out * dout[:, None].float()).sum(2)
-        dlogits = gmi.moe_route_bwd(logits, r.indices, r.weights, r.offsets, r.live, dweights, dloss, mask=rows[0])
+        h, y, logits, r, _, (mask, a, d) = saved
+        if through_experts:
+            q, s, dweights = gmi.moe_unpermute_bwd(dout, r.slot_row, weights=r.weights, rows=d, quantize=True)
+        else:
+            _, dweights = gmi.moe_unpermute_bwd(dout, r.slot_row, weights=r.weights, rows=d, row_grad=False)
+        dlogits = gmi.moe_route_bwd(logits, r.indices, r.weights, r.offsets, r.live, dweights, dloss, mask=mask)
         dy = dlogits @ self.router
         if through_experts:
-            dy = (dy.float() + self.experts_backward(dout, r, rows)).to(dy.dtype)
+            # the experts' data gradient: the transposed products (the roundings to fp8 have no derivative)
+            dact = gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.down_t)
+            q, s = gmi.swiglu_bwd(dact, a, live=r.offsets[-1:], quantize=True)
+            dy = gmi.moe_unpermute(gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.up_t), r.slot_row, add=dy, out=dy)
         dh, dnorm = gmi.rmsnorm_bwd(dy, h, self.norm, dres=dh_out)
         return dh, dnorm, dlogits.t().contiguous() @ y
-
-    def experts_backward(self, dout, r, rows):
-        """Gradient of the experts' input, float32 [tokens][hidden] (the roundings to fp8 have no derivative)."""
-        _, token, routed, a = rows
-        share = torch.where(routed, r.weights.view(-1)[r.row_slot.clamp_min(0).long()], 0.0)
-        q, s = quantize(dout[token].float() * share[:, None])
-        dact = gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.down_t).float()
-        gate, up = a[:, : self.inner].float(), a[:, self.inner:].float()
-        sig = torch.sigmoid(gate)
-        da = torch.cat([dact * up * sig * (1.0 + gate * (1.0 - sig)), dact * gate * sig], 1)
-        q, s = quantize(torch.where(routed[:, None], da, 0.0))
-        dx = gmi.gemm_f8_block_grouped(r.offsets, q, s, *self.up_t)
-        return torch.where(r.slot_row[..., None] >= 0, dx[r.slot_row.clamp_min(0).long()].float(), 0.0).sum(1)
 
 
 def main():
@@ -117,7 +109,7 @@ def main():
     dloss = torch.tensor([0.01], device="cuda")
 
     def step():
-        out, h, saved = layer.forward(x, res)
+        out, h, saved = layer.forward(x, res, per_slot=False)
         return saved[3], layer.backward(dout, dloss, saved, dh_out=dout, through_experts=True)
 
     for _ in range(3):

@@ -654,13 +654,21 @@ def moe_unpermute(rows: torch.Tensor, slot_row: torch.Tensor, weights: torch.Ten
 def moe_unpermute_bwd(dout: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor | None = None,
                       rows: torch.Tensor | None = None, drows: torch.Tensor | None = None,
                       scales: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
-                      quantize: bool = False, stream=None):
+                      quantize: bool = False, stream=None, row_grad: bool = True):
     """Gradients of moe_unpermute: drows[slot_row[t, i]] = weights[t, i] * dout[t], in dout's type or with
     quantize=True as float8_e4m3fn with `scales` float32 [n][ceil(K / 128)], and dweights[t, i] = <dout[t],
     rows[slot_row[t, i]]> float32 where `rows` (what the forward call read) is given.  Returns (drows, dweights), or
-    (drows, scales, dweights) with quantize; dweights is None without rows.  Rows that no slot has are not written."""
-    if rows is None and dweights is not None:
+    (drows, scales, dweights) with quantize; dweights is None without rows.  Rows that no slot has are not written.
+    With row_grad=False (nothing behind the rows is trained) drows and scales are None."""
+    if rows is None and (dweights is not None or not row_grad):
         raise ValueError("dweights needs the rows of the forward call")
+    if not row_grad:
+        if drows is not None or scales is not None or quantize:
+            raise ValueError("drows and scales are written with row_grad=True only")
+        if dweights is None:
+            dweights = _new(slot_row.shape, torch.float32, dout.device, stream)
+        _check(_bound().moe_unpermute_bwd(dout, slot_row, weights, rows, None, None, None, dweights, stream))
+        return None, dweights
     if scales is not None and not quantize:
         raise ValueError("scales are written with quantize=True only")
     n = slot_row.numel() if rows is None else rows.shape[0]

@@ -1222,10 +1222,11 @@ gmi_status gmi_moe_unpermute_bwd(int32_t tokens, int32_t k, int32_t K, gmi_dtype
   if (st != GMI_OK || tokens == 0) return st;
   if ((st = row_operand(who, "dout", dout, lddout, K)) != GMI_OK || (st = slot_rows(who, slot_row)) != GMI_OK)
     return st;
-  if ((drows == nullptr) == (q == nullptr && scales == nullptr) && rows > 0)
-    return fail(GMI_ERR_INVALID_ARG, "%s: either drows or q with scales", who);
-  if (rows > 0 && (drows ? (st = row_operand(who, "drows", drows, lddrows, K)) : (st = code_operand(who, q, ldq, scales, lds, K))) != GMI_OK)
-    return st;
+  const bool coded = q || scales;
+  if (rows > 0 && ((drows && coded) || (!drows && !coded && !dweights)))
+    return fail(GMI_ERR_INVALID_ARG, "%s: drows, or q with scales, or dweights alone", who);
+  if (rows > 0 && drows && (st = row_operand(who, "drows", drows, lddrows, K)) != GMI_OK) return st;
+  if (rows > 0 && coded && (st = code_operand(who, q, ldq, scales, lds, K)) != GMI_OK) return st;
   if (dweights && rows > 0 && (st = row_operand(who, "y", y, ldy, K)) != GMI_OK) return st;
   if (!aligned(weights, 4) || !aligned(dweights, 4))
     return fail(GMI_ERR_MISALIGNED, "%s: weights and dweights must be 4-byte aligned", who);

@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void k_unpermute_bwd(UnpermuteBwdLaunch a) {
               if (own >> ((lane & 48) + i) & 1) q = codes8(g, block_scale(fabsf(wi) * m));
             }
             store<NT>(a.q + r * a.ldq + (int64_t)c * 8, q);
-          } else {
+          } else if (a.drows) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = wi * d[e];
             store<NT>(a.drows + r * a.lddr + (int64_t)c * 8, pack8<DT>(g));

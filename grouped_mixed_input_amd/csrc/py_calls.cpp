@@ -467,8 +467,8 @@ PyObject* moe_unpermute_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Slots s = slots_of(at, a[1]);
     if (s.T != d.rows) refuse("dout and slot_row disagree on the tokens");
     const float* w = at.vector<float>(a[2], "weights", s.T * s.k, F32);
-    PyObject* first = a[4] != Py_None ? a[4] : a[5];
-    const at::Tensor& ft = tensor(first, "drows or q");
+    PyObject* first = a[4] != Py_None ? a[4] : a[5] != Py_None ? a[5] : a[3];
+    const at::Tensor& ft = tensor(first, "drows, q or rows");
     const int64_t rows = ft.dim() ? ft.size(0) : 0;
     const Matrix y = at.matrix_or_none(a[3], "rows", rows, d.cols, d.type),
                  dr = at.matrix_or_none(a[4], "drows", rows, d.cols, d.type),

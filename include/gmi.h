@@ -612,7 +612,8 @@ gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dty
  *   y          as the forward read it; needed with dweights only.
  *   drows      [rows][lddrows], `dtype`; or NULL, and q fp8 [rows][ldq] (8-byte
  *              aligned, ldq a multiple of 8, of 16 where a GEMM call reads it)
- *              with scales fp32 [rows][lds].  drows may be y exactly.
+ *              with scales fp32 [rows][lds]; or none of them (dweights alone).
+ *              drows may be y exactly.
  *   dweights   fp32 [tokens][k] or NULL (a frozen router).
  * A NaN among g stands in q and does not enter the block's maximum.  Rows that
  * no slot has are not written.  Sizes as for gmi_moe_unpermute. */

@@ -78,7 +78,7 @@ def test_unpermute_bwd_refusals(gmi):
     bad, uns, mis = kinds(gmi)
     wide = dict(q=None, s=None, dr=A16 * 9, lddr=256)
     refused(call, bad, [dict(T=-1), dict(k=0), dict(K=0), dict(rows=-1), dict(d=None), dict(sr=None), dict(y=None),
-                        dict(ldd=8), dict(ldy=8), dict(q=None), dict(s=None), dict(q=None, s=None), dict(dr=A16 * 9, lddr=256),
+                        dict(ldd=8), dict(ldy=8), dict(q=None), dict(s=None), dict(q=None, s=None, dw=None), dict(dr=A16 * 9, lddr=256),
                         dict(ldq=248), dict(lds=1), dict(wide, lddr=248)])
     refused(call, uns, [dict(k=17), dict(dt=2), dict(dt=3), dict(T=2 ** 30, k=2)])
     refused(call, mis, [dict(K=252), dict(d=A16 + 8), dict(y=A16 + 8), dict(ldd=260), dict(ldy=260), dict(q=A16 + 4),
@@ -154,6 +154,8 @@ def test_binding_refuses_wrong_tensors(gmi):
     no("device", gmi.moe_unpermute_bwd, x, slots)
     no("rows of the forward", gmi.moe_unpermute_bwd, x, slots, dweights=torch.zeros(4, 2))
     no("quantize=True", gmi.moe_unpermute_bwd, x, slots, scales=torch.zeros(8, 2))
+    no("row_grad=True", gmi.moe_unpermute_bwd, x, slots, rows=x, drows=x, row_grad=False)
+    no("rows of the forward", gmi.moe_unpermute_bwd, x, slots, row_grad=False)
     no("device", gmi.swiglu_quant, x)
     no("quantize=True", gmi.swiglu_quant, x, q=x, quantize=False)
     no("device", gmi.swiglu_bwd, x[:, :128], x)

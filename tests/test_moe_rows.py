@@ -179,6 +179,16 @@ def test_unpermute_bwd_without_weights_or_rows(gmi, quant):
         assert torch.equal(got[0].cpu().double(), d)
 
 
+def test_unpermute_bwd_of_the_weights_alone(gmi):
+    gen = torch.Generator().manual_seed(11)
+    slot_row = ref.slots(gen, 300, 4, 3).to(dev())
+    y, dout = (torch.randn(n, 520, generator=gen).to(torch.bfloat16).to(dev()) for n in (1203, 300))
+    keep = y.clone()
+    drows, dw = gmi.moe_unpermute_bwd(dout, slot_row, rows=y, row_grad=False)
+    _, want = gmi.moe_unpermute_bwd(dout, slot_row, rows=y)
+    assert drows is None and same(dw, want) and same(y, keep)
+
+
 def test_unpermute_bwd_over_the_rows_it_reads(gmi):
     # the rows' gradient in the place of the rows
     gen = torch.Generator().manual_seed(9)
