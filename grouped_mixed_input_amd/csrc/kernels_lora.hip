@@ -325,6 +325,10 @@ template <bool LONG, int DT, int RS, bool ONE>
 __device__ __forceinline__ void load_t(const LoraLaunch& a, int64_t pos, bool in, LoraT<DT, RS, ONE>& t) {
   const int lane = threadIdx.x & 63, kg = lane >> 4;
   const int64_t run = (int64_t)a.M * a.rank;
+  // Runs of K whose sums are read together.  Eight of ranks above 64 spill in the
+  // kernel with the rings (1024 rows, rank 128: 81 us; four 25, two 27, one 33);
+  // up to 64 ranks eight cost nothing.
+  constexpr int AT = RS > 2 ? 4 : 8;
   float v[RS][8];
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
@@ -333,7 +337,7 @@ __device__ __forceinline__ void load_t(const LoraLaunch& a, int64_t pos, bool in
     if (in && col < a.rank) {
       const int first = ONE ? kg >> 1 : 0, every = ONE ? 2 : 1;
       const float* p = a.part + part_at<LONG>(a, pos, col) + first * run;
-#pragma unroll 8
+#pragma unroll AT
       for (int q = first; q < a.splits; q += every) {
         s0 += *(const f32x4*)p;
         s1 += *(const f32x4*)(p + (LONG ? 4 * (int64_t)a.M : 4));
