@@ -1321,7 +1321,8 @@ gmi_status gmi_swiglu_bwd(int32_t rows, int32_t N, gmi_dtype dtype, const void* 
 // ---------------------------------------------------------------------------
 // low-rank adapters beside a dense product
 // ---------------------------------------------------------------------------
-constexpr int32_t kMaxLoraRows = int32_t(1) << 29;  // a launch's threads stay below 2^32
+// tiles of 64 rows, up to eight workgroups of 256 threads each where tiles are many: below 2^32 threads a launch
+constexpr int32_t kMaxLoraRows = int32_t(1) << 26;
 
 size_t gmi_gemm_lora_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t rank) {
   if (M <= 0 || N <= 0 || K <= 0 || rank <= 0 || rank > kMaxLoraRank || M > kMaxLoraRows) return 0;
@@ -1339,9 +1340,10 @@ gmi_status gmi_gemm_lora(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t 
     return fail(GMI_ERR_INVALID_ARG, "%s: M %d, N %d, K %d, rank %d, adapters %d", who, M, N, K, rank, adapters);
   if (!dtype_ok(dtype)) return fail(GMI_ERR_UNSUPPORTED, "%s: dtype %d not supported", who, (int)dtype);
   if (rank > kMaxLoraRank) return fail(GMI_ERR_UNSUPPORTED, "%s: rank %d above %d", who, rank, kMaxLoraRank);
-  if (M > kMaxLoraRows) return fail(GMI_ERR_UNSUPPORTED, "%s: M above 2^29", who);
-  if (N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
-    return fail(GMI_ERR_UNSUPPORTED, "%s: N or K not below 2^31 - 2^10", who);
+  if (M > kMaxLoraRows) return fail(GMI_ERR_UNSUPPORTED, "%s: M above 2^26", who);
+  // (at most 512 parts of columns, each rounded up to 256, and 16 of K to 64: their ends are 32-bit numbers)
+  if (N > INT32_MAX - (1 << 18) || K > INT32_MAX - (1 << 18))
+    return fail(GMI_ERR_UNSUPPORTED, "%s: N or K not below 2^31 - 2^18", who);
   if (N % 8 || K % 8 || rank % 8)
     return fail(GMI_ERR_MISALIGNED, "%s: N, K and rank must be multiples of 8 (128-bit accesses)", who);
   if (M == 0 || N == 0) return GMI_OK;

@@ -659,7 +659,7 @@ size_t gmi_gemm_lora_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t ra
  * whose index lies outside [0, adapters) gets base (zeros without one).
  *   X, base, Y  [M][ldx], [M][ldbase], [M][ldy]; A, B: dtype GMI_F16 or GMI_BF16.
  *   N, K, rank  multiples of 8; rank 1 .. 128 (pad smaller adapters with
- *            zeros); M at most 2^29.
+ *            zeros); M at most 2^26, N and K below 2^31 - 2^18.
  *   scales   fp32 [adapters] or NULL for 1.
  *   index    int32 [M].
  *   order    int32 [M], the rows in an order that brings those of one adapter

@@ -124,6 +124,8 @@ def test_lora_refusals(gmi):
                         dict(ldy=248), dict(sa=8184), dict(sb=4088), dict(sa=-8192), dict(base=A16 * 8, ldbase=264)])
     refused(call, uns, [dict(dt=2), dict(dt=3), dict(rank=136), dict(M=(1 << 29) + 1), dict(N=2 ** 31 - 8, ldy=2 ** 31 - 8),
                         dict(K=2 ** 31 - 8)])
+    # more workgroups than a launch holds; ends of parts past 32 bits
+    refused(call, uns, [dict(M=(1 << 26) + 1), dict(N=2 ** 31 - 2 ** 18, ldy=2 ** 31), dict(K=2 ** 31 - 2 ** 18)])
     refused(call, mis, [dict(N=252), dict(K=508), dict(rank=12), dict(X=A16 + 8), dict(A=A16 + 8), dict(B=A16 + 8),
                         dict(base=A16 + 8), dict(Y=A16 + 8), dict(ldx=516), dict(lda=516), dict(ldb=20), dict(ldbase=260),
                         dict(ldy=260), dict(sa=8196), dict(sb=4100), dict(s=A16 + 2), dict(index=A16 + 2), dict(order=A16 + 2),
