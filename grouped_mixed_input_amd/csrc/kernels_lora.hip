@@ -308,8 +308,8 @@ __global__ __launch_bounds__(256) void k_lora_down_long(LoraLaunch a, int tiles,
 // again as its own rounding, so T goes in as two terms, t = hi + lo, whose
 // products with B are summed: what is lost is 2^-17 (bf16) or 2^-22 (fp16) of
 // t.  fp16 cannot hold every t: a row is scaled by the power of two that brings
-// its largest to [1, 2), and `f` takes it back.  Up to rank 16 both terms fit
-// one instruction (k 0..15 hi, 16..31 lo, against B twice).
+// its largest, infinities aside, to [1, 2), and `f` takes it back.  Up to rank 16
+// both terms fit one instruction (k 0..15 hi, 16..31 lo, against B twice).
 template <int DT, int RS, bool ONE>
 struct LoraT {
   u32x4 hi[RS], lo[ONE ? 1 : RS];
@@ -363,14 +363,12 @@ __device__ __forceinline__ void load_t(const LoraLaunch& a, int64_t pos, bool in
 #pragma unroll
     for (int r = 0; r < RS; ++r)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[r][e]));
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[r][e]) < __builtin_inff() ? fabsf(v[r][e]) : 0.0f);
     m = max4(m);
-    // 2^(exponent of m), inside the normal range with its reciprocal; rows that
-    // hold an infinity stay as they are
+    // 2^(exponent of m), inside the normal range with its reciprocal
     const uint32_t ex = min(max(__builtin_bit_cast(uint32_t, m) >> 23, 2u), 252u);
-    const bool scale = m < __builtin_inff();
-    t.f = scale ? __builtin_bit_cast(float, ex << 23) : 1.0f;
-    const float inv = scale ? __builtin_bit_cast(float, (254u - ex) << 23) : 1.0f;
+    t.f = __builtin_bit_cast(float, ex << 23);
+    const float inv = __builtin_bit_cast(float, (254u - ex) << 23);
 #pragma unroll
     for (int r = 0; r < RS; ++r)
 #pragma unroll

@@ -655,7 +655,8 @@ size_t gmi_gemm_lora_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t ra
  *   Y[m] = RN(base[m] + scales[a] * (X[m] A_a^T) B_a^T),  a = index[m]
  * with A_a = A + a * a_stride [rank][lda] and B_a = B + a * b_stride [N][ldb].
  * Sums are fp32; X A^T enters the second product as two terms of the type,
- * together good to 2^-17 (bf16) or 2^-22 (fp16) of a row's largest.  A row
+ * together good to 2^-17 (bf16) or 2^-22 (fp16) of a row's largest; an
+ * infinity in B may therefore give NaN where it would give an infinity.  A row
  * whose index lies outside [0, adapters) gets base (zeros without one).
  *   X, base, Y  [M][ldx], [M][ldbase], [M][ldy]; A, B: dtype GMI_F16 or GMI_BF16.
  *   N, K, rank  multiples of 8; rank 1 .. 128 (pad smaller adapters with

@@ -102,6 +102,21 @@ def test_lora_fp16_holds_products_past_its_range(gmi, sx, sa):
     check(gmi.gemm_lora(*d[:4], scales=d[4]), X, A, B, index, scales, None)
 
 
+@pytest.mark.parametrize("M", [40, 600])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_lora_infinity_beside_products_past_the_type(gmi, dtype, M):
+    # one row of A holds an infinity: X A^T is infinite in that column and about 2^20 in the others, whose sums of
+    # either sign leave the infinity as it is
+    rank, K, N = 24, 128, 72
+    X, A = torch.full((M, K), 64.0), torch.full((1, rank, K), 128.0)
+    A[0, 3, 5] = math.inf
+    B = torch.where(torch.arange(rank) % 2 == 0, -1.0, 1.0).expand(1, N, rank).clone()
+    B[0, 7::2] *= -1
+    index = torch.zeros(M, dtype=torch.int32)
+    got = gmi.gemm_lora(*up(X.to(dtype), A.to(dtype), B.to(dtype), index)).cpu().float()
+    assert torch.equal(got, (B[0, :, 3] * math.inf).expand(M, N))
+
+
 def test_lora_odd_orders(gmi):
     # rows left out of the order, entries that are no rows, adapters past the last: base, or as they were
     X, A, B, index, scales, base = case(70, 72, 128, 8, 4, torch.float16, none=0.0)
