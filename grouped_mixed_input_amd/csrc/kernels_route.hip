@@ -487,6 +487,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int w
 // group are a group of their own behind the others, whose counts go nowhere.
 // With one workgroup the places follow at once; otherwise the ranks wait in
 // `place` for k_group_place.
+// Latency bounds it: 64 rows 2.7 us (an empty launch 2.5), 131072 rows into 128
+// groups 3.8 and 6.7 in the second launch.
 __global__ __launch_bounds__(RT_THREADS) void k_group(GroupLaunch a) {
   __shared__ uint16_t hist[RT_THREADS / 64][kMaxGroups + 8];
   __shared__ int base[kMaxGroups + 8];
@@ -552,6 +554,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_group(GroupLaunch a) {
   }
 }
 
+// Every workgroup sums the count matrix for itself, as k_route_place does, and
+// turns its rows' ranks into places.
 __global__ __launch_bounds__(RT_THREADS) void k_group_place(GroupLaunch a, int wgs) {
   __shared__ int32_t part[2][8 * RT_THREADS];
   __shared__ int row0[kMaxGroups + 1];
@@ -736,9 +740,11 @@ hipError_t launch_route_bwd(const RouteBwdLaunch& a, int dtype, hipStream_t stre
 
 GroupPlan plan_group(int n, int G) {
   GroupPlan p;
-  // one launch up to four passes of a workgroup; then 256 workgroups, whose counts have 16 bits
+  // One launch up to two passes of a workgroup (2048 rows into 128 groups 6.4 us,
+  // two launches 8.5; four passes, 4096 rows, 10.8 against 8.6); then 256
+  // workgroups, whose counts have 16 bits
   const int64_t passes = ((int64_t)n + RT_THREADS - 1) / RT_THREADS;
-  const int64_t per = passes <= 4 ? std::max<int64_t>(passes, 1)
+  const int64_t per = passes <= 2 ? std::max<int64_t>(passes, 1)
                                   : std::min<int64_t>((passes + 255) / 256, 65535 / RT_THREADS);
   p.rows_per_wg = (int)(per * RT_THREADS);
   p.wgs = (int)std::max<int64_t>((passes + per - 1) / per, 1);

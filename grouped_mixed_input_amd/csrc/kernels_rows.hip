@@ -13,6 +13,12 @@
 // each output written once, 16 bytes a lane.  The walk is by token, so a
 // token's row (or gradient) is fetched once for its k experts, and the sum over
 // k has a fixed order.
+//
+// 16384 tokens, top 8, 4096 columns: permute (fp8) 106 to 111 us (5.6 to 5.9
+// TB/s), unpermute (bf16, with add) 242 (5.55), its gradient as codes 334 (5.3);
+// 131072 x 2 x 1024 bf16: gate 110 us (6.1 TB/s), its gradient 164 (6.4), where
+// arithmetic takes as long as memory.  Rows of 4 KB far apart cost 15% over a
+// contiguous walk.  Few tokens: 3.6 us a launch, of which an empty one takes 2.5.
 #include "gmi_device.hpp"
 #include "gmi_internal.hpp"
 #include "gmi_rows.hpp"

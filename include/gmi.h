@@ -51,7 +51,7 @@ typedef enum {
   GMI_ERR_HIP = 5          /* a HIP runtime call or kernel launch failed   */
 } gmi_status;
 
-/* Element types.  GMI_F8E4M3 (GEMM calls only): A and B are OCP fp8 E4M3
+/* Element types.  GMI_F8E4M3 (GEMM calls and gmi_moe_permute): A and B are OCP fp8 E4M3
  * (1 sign, 4 exponent bits with bias 7, 3 mantissa bits, no infinities,
  * S.1111.111 is NaN, largest finite 448), C and D are bf16; the product of
  * two fp8 values and their sum are formed exactly in fp32 by the matrix
@@ -558,7 +558,7 @@ gmi_status gmi_moe_route_bwd(int32_t tokens, int32_t experts, int32_t k, const v
  * written for it.  No two slots may share a row.
  * ------------------------------------------------------------------------ */
 
-/* Bytes of the workspace gmi_group_rows needs (0 for up to 4096 rows). */
+/* Bytes of the workspace gmi_group_rows needs (0 for up to 2048 rows). */
 size_t gmi_group_rows_workspace_bytes(int32_t n, int32_t groups);
 
 /* Rows ordered by a number that each carries (its expert, its adapter), for

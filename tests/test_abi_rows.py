@@ -38,7 +38,7 @@ def test_group_rows_refusals(gmi):
     need = gmi.lib().gmi_group_rows_workspace_bytes(5000, 8)
     assert need > 0
     refused(call, gmi.GMI_ERR_WORKSPACE, [dict(ws=None), dict(nbytes=need - 1), dict(n=2 ** 31 - 2 ** 17 - 1, nbytes=0)])
-    for n, g in ((4096, 8), (0, 8), (-1, 8), (5000, 0), (5000, 1025)):
+    for n, g in ((2048, 8), (0, 8), (-1, 8), (5000, 0), (5000, 1025)):
         assert gmi.lib().gmi_group_rows_workspace_bytes(n, g) == 0
 
 

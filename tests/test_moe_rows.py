@@ -25,7 +25,7 @@ def same(a, b):
 
 # ---------------------------------------------------------------- group_rows
 @pytest.mark.parametrize("n,groups", [(0, 3), (1, 1), (2, 7), (63, 5), (64, 16), (65, 1024), (1023, 60), (1024, 2),
-                                      (1025, 128), (4096, 1023), (4097, 9), (5000, 1024), (40000, 128), (300001, 37)])
+                                      (1025, 128), (2048, 300), (2049, 300), (4096, 1023), (4097, 9), (5000, 1024), (40000, 128), (300001, 37)])
 def test_group_rows(gmi, n, groups):
     gen = torch.Generator().manual_seed(n + groups)
     index = torch.randint(-2, groups + 2, (n,), generator=gen).to(torch.int32)
