@@ -1,7 +1,7 @@
 // kernels_lora.hip -- low-rank adapters of many requests beside one dense
 // product: Y[m] = base[m] + s_a (X[m] A_a^T) B_a^T with the row's own adapter a.
 //
-// Two launches: T = X A^T over runs of K (fp32 partial sums, added in order),
+// Two launches: T = X A^T over runs of K (fp32 partial sums, added in one order),
 // then Y from T.  Both walk tiles of 64 rows in the order of the call.
 // Neighbouring rows of one adapter form a run, and a run is the unit of work:
 // its rows are the columns of 16 x 16 x 32 matrix instructions, 16 at a time,
@@ -13,12 +13,12 @@
 // have a row or two: latency counts); from 512 on through rings in LDS, copied
 // in whole lines.  8192 x 8192, rank 64, 8 adapters, us of both kernels, through
 // registers / through LDS: 256 rows (rank 16) 13.2 / 16.2, 512 rows 35 / 28, 1024
-// rows 38 / 28, 4096 rows 90 / 60.
+// rows 38 / 26, 4096 rows 90 / 60.
 //
 // Bound by memory and by what a launch takes to start (a first copy waits for
-// the row's place, then for its adapter's number): 4096 rows 23 + 37 us, the
-// second at 4.5 TB/s past the 7 us that it needs for any size; 16 rows of 16
-// adapters, rank 16, 4.3 + 5.6.
+// the row's place, then for its adapter's number): 4096 rows 22.9 + 37.4 us, the
+// second at 4.9 TB/s past the 7 us that it needs for any size; 16 rows of 16
+// adapters, rank 16, 4.3 + 5.4.
 #include <algorithm>
 
 #include "gmi_device.hpp"
@@ -60,6 +60,7 @@ __device__ __forceinline__ int64_t part_at(const LoraLaunch& a, int64_t pos, int
   return LONG ? ((int64_t)(col >> 2) * a.M + pos) * 4 : pos * a.rank + col;
 }
 
+constexpr int kMostSplits = 16, kLongSplits = 8;  // runs of K; past rank 16 in the kernels for long runs
 // 16 bytes, or zeros
 __device__ __forceinline__ u32x4 load_if(const uint16_t* p, bool in) { return in ? *(const u32x4*)p : u32x4{}; }
 
@@ -319,44 +320,83 @@ __device__ __forceinline__ float max4(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));
 }
-// With ONE lanes 32 apart hold the same columns: each sums every other run of K,
-// and they add up (16 runs 1 latency of memory, not 4).
-template <bool LONG, int DT, int RS, bool ONE>
-__device__ __forceinline__ void load_t(const LoraLaunch& a, int64_t pos, bool in, LoraT<DT, RS, ONE>& t) {
-  const int lane = threadIdx.x & 63, kg = lane >> 4;
-  const int64_t run = (int64_t)a.M * a.rank;
-  // Runs of K whose sums are read together.  Eight of ranks above 64 spill in the
-  // kernel with the rings (1024 rows, rank 128: 81 us; four 25, two 27, one 33);
-  // up to 64 ranks eight cost nothing.
-  constexpr int AT = RS > 2 ? 4 : 8;
-  float v[RS][8];
+// C quarters of the sum over the runs of K from the j-th on; quarter q holds the
+// runs q, q + 4, ..., at most R of them, and two quarters are added before two
+// pairs are.  With ONE lanes 32 apart hold the same columns, and each sums every
+// other run of a quarter.  Loads are on their way together; past the last run it
+// is read again and not added.
+template <bool LONG, int RS, bool ONE, int C, int R>
+__device__ __forceinline__ void sum_rounds(const LoraLaunch& a, int64_t pos, bool in, int j, float (&v)[RS][8]) {
+  // places of a lane on their way (128 rows, rank 128, the second kernel: 17.1 us, with
+  // four 18.4; long runs with 16: 512 rows, rank 64, 17.9 for 18.4, 1024, rank 128, 22.5 for 21.4)
+  constexpr int MOST = 8;
+  constexpr int AT = C * R <= MOST ? R : MOST / C, RG = C * AT * RS <= MOST ? RS : MOST / (C * AT);  // runs, rank tiles
+  const int kg = (threadIdx.x & 63) >> 4, every = ONE ? 8 : 4;
+  const int64_t run = (int64_t)a.M * a.rank, beside = LONG ? 4 * (int64_t)a.M : 4;
+  j += ONE ? 4 * (kg >> 1) : 0;
 #pragma unroll
-  for (int r = 0; r < RS; ++r) {
-    const int col = ONE ? 8 * (kg & 1) : 32 * r + 8 * kg;
-    f32x4 s0{}, s1{};
-    if (in && col < a.rank) {
-      const int first = ONE ? kg >> 1 : 0, every = ONE ? 2 : 1;
-      const float* p = a.part + part_at<LONG>(a, pos, col) + first * run;
-#pragma unroll AT
-      for (int q = first; q < a.splits; q += every) {
-        s0 += *(const f32x4*)p;
-        s1 += *(const f32x4*)(p + (LONG ? 4 * (int64_t)a.M : 4));
-        p += every * run;
+  for (int r0 = 0; r0 < RS; r0 += RG) {
+    float sum[RG][C][8];
+    bool there[RG];
+    const float* p[RG];
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      const int col = ONE ? 8 * (kg & 1) : 32 * (r0 + r) + 8 * kg;
+      there[r] = in && col < a.rank;
+      p[r] = there[r] ? a.part + part_at<LONG>(a, pos, col) : a.part;
+    }
+#pragma unroll
+    for (int q0 = 0; q0 < R; q0 += AT) {
+      f32x4 s[RG][C][AT][2];
+#pragma unroll
+      for (int r = 0; r < RG; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int q = 0; q < AT; ++q) {
+            const int64_t at = min(j + c + (q0 + q) * every, a.splits - 1) * run;
+            s[r][c][q][0] = *(const f32x4*)(p[r] + at);
+            s[r][c][q][1] = *(const f32x4*)((there[r] ? p[r] + beside : p[r]) + at);
+          }
+#pragma unroll
+      for (int r = 0; r < RG; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (q0 == 0) sum[r][c][e] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < AT; ++q)
+              sum[r][c][e] += there[r] && j + c + (q0 + q) * every < a.splits ? s[r][c][q][e / 4][e % 4] : 0.0f;
+          }
+    }
+#pragma unroll
+    for (int r = 0; r < RG; ++r)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (ONE) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) sum[r][c][e] += __shfl_xor(sum[r][c][e], 32);
+        }
+        if constexpr (C == 1) v[r0 + r][e] = sum[r][0][e];
+        else if constexpr (C == 2) v[r0 + r][e] = sum[r][0][e] + sum[r][1][e];
+        else v[r0 + r][e] = (sum[r][0][e] + sum[r][1][e]) + (sum[r][2][e] + sum[r][3][e]);
       }
-    }
-    if constexpr (ONE) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s0[e] += __shfl_xor(s0[e], 32);
-        s1[e] += __shfl_xor(s1[e], 32);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[r][e] = s0[e];
-      v[r][4 + e] = s1[e];
-    }
+    __builtin_amdgcn_sched_barrier(0);  // the next ranks' loads would spill
   }
+}
+template <bool LONG, int RS, bool ONE, int C>
+__device__ __forceinline__ void sum_t(const LoraLaunch& a, int64_t pos, bool in, int j, float (&v)[RS][8]) {
+  const int rounds = (a.splits + (ONE ? 7 : 3)) / (ONE ? 8 : 4);
+  static_assert(kLongSplits <= 8 && kMostSplits <= 16);
+  if (C > 1 && a.splits == 1) sum_rounds<LONG, RS, ONE, 1, 1>(a, pos, in, j, v);
+  else if (rounds <= 1) sum_rounds<LONG, RS, ONE, C, 1>(a, pos, in, j, v);
+  else if (ONE || rounds <= 2) sum_rounds<LONG, RS, ONE, C, 2>(a, pos, in, j, v);
+  else if constexpr (!LONG && !ONE) sum_rounds<LONG, RS, ONE, C, kMostSplits / 4>(a, pos, in, j, v);
+}
+template <int DT, int RS, bool ONE>
+__device__ __forceinline__ void split_t(float (&v)[RS][8], LoraT<DT, RS, ONE>& t) {
+  const int kg = (threadIdx.x & 63) >> 4;
   t.f = 1.0f;
   if constexpr (DT == DT_F16) {
     float m = 0.0f;
@@ -425,16 +465,24 @@ __device__ __forceinline__ void lora_columns(const u32x4 (&b)[RS][4], const Lora
   }
 }
 
+template <int DT, int RS, bool ONE>
+union LoraUpLds {
+  LoraT<DT, RS, ONE> t[4][64];  // past 16 rows
+  f32x4 part[4][RS][2][64];     // up to 16
+};
 // Y of one short run: a wave makes 64 columns of up to 64 rows at a time.  B is
 // the instruction's first operand, its rows dealt so that a lane ends with eight
 // neighbouring columns of one row of Y twice: row i of instruction m is column
 // 32 (m / 2) + 8 (i / 4) + 4 (m % 2) + i % 4, and a lane's results are columns
 // 32 (m / 2) + 8 (l / 16) + 4 (m % 2) + j.  B and base are asked for before T,
-// which comes of the longer way.  Past 16 rows each wave makes T of 16 of them
-// for all, through LDS.
+// which comes of the longer way: up to 16 rows a wave sums a quarter of the runs of
+// K and the quarters meet in LDS, so that 16 runs cost one trip to memory (78 rows
+// 1432 x 4296, rank 64: 11.4 us with four trips, 8.3; 128 rows 8192 x 8192, rank
+// 128: 21 and 17).  Past 16 rows each wave makes T of 16 of them for all, in the
+// same order of the sum.
 template <int DT, int RS, bool ONE, int NS>
 __device__ __forceinline__ void lora_up(const LoraLaunch& a, const LoraTile& t, int tile, int p0, int p1, int n0,
-                                        int n1, LoraT<DT, RS, ONE> (*shared)[64]) {
+                                        int n1, LoraUpLds<DT, RS, ONE>& lds) {
   const int lane = threadIdx.x & 63, wave = wave_id(), i16 = lane & 15, kg = lane >> 4;
   const int id = __builtin_amdgcn_readlane(t.id, p0);
   const uint16_t* b = a.B + id * a.b_stride;
@@ -468,16 +516,42 @@ __device__ __forceinline__ void lora_up(const LoraLaunch& a, const LoraTile& t, 
   int c0 = n0 + 64 * wave;
   if (c0 < n1) fetch(c0);
   const float scale = a.scales ? a.scales[id] : 1.0f;
-  const int64_t pos = (int64_t)tile * LO_ROWS + p0 + i16;
+  const int p = p0 + (NS == 1 ? 0 : 16 * wave) + i16;
+  const int64_t pos = (int64_t)tile * LO_ROWS + p;
+  float v[RS][8];
   LoraT<DT, RS, ONE> t0;
   if constexpr (NS == 1) {
-    load_t<false>(a, pos, in[0], t0);
+    sum_t<false, RS, ONE, 1>(a, pos, p < p1, wave, v);
+#pragma unroll
+    for (int r = 0; r < RS; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        lds.part[wave][r][h][lane] = f32x4{v[r][4 * h], v[r][4 * h + 1], v[r][4 * h + 2], v[r][4 * h + 3]};
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RS; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 s = (lds.part[0][r][h][lane] + lds.part[1][r][h][lane]) +
+                        (lds.part[2][r][h][lane] + lds.part[3][r][h][lane]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[r][4 * h + e] = s[e];
+      }
+    split_t(v, t0);
     t0.f *= scale;
   } else {
     if (wave < NS) {
-      load_t<false>(a, pos + 16 * wave, p0 + 16 * wave + i16 < p1, t0);
+      // (two quarters at a time: with four the kernel takes the registers of two waves)
+      float w[RS][8];
+      sum_t<false, RS, ONE, 2>(a, pos, p < p1, 0, v);
+      sum_t<false, RS, ONE, 2>(a, pos, p < p1, 2, w);
+#pragma unroll
+      for (int r = 0; r < RS; ++r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[r][e] += w[r][e];
+      split_t(v, t0);
       t0.f *= scale;
-      shared[wave][lane] = t0;
+      lds.t[wave][lane] = t0;
     }
     __syncthreads();
   }
@@ -488,7 +562,7 @@ __device__ __forceinline__ void lora_up(const LoraLaunch& a, const LoraTile& t, 
       if constexpr (NS == 1)
         tv = t0;
       else
-        tv = shared[s][lane];
+        tv = lds.t[s][lane];
       u32x4 o[2];
       lora_columns(bv, tv, base[s], o);
 #pragma unroll
@@ -498,7 +572,7 @@ __device__ __forceinline__ void lora_up(const LoraLaunch& a, const LoraTile& t, 
     c0 += 256;
     if (c0 < n1) fetch(c0);
   }
-  if constexpr (NS > 1) __syncthreads();  // the next run's T may come
+  __syncthreads();  // the next run's T may come
 }
 
 // rows without an adapter: base, or zeros
@@ -594,7 +668,9 @@ __device__ __forceinline__ void lora_up_long(const LoraLaunch& a, const LoraTile
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) fetch(i);
   LoraT<DT, RS, ONE> tv;
-  load_t<true>(a, (int64_t)tile * LO_ROWS + p0 + 16 * wave + i16, p0 + 16 * wave + i16 < p1, tv);
+  float tsum[RS][8];
+  sum_t<true, RS, ONE, 4>(a, (int64_t)tile * LO_ROWS + p0 + 16 * wave + i16, p0 + 16 * wave + i16 < p1, 0, tsum);
+  split_t(tsum, tv);
   tv.f *= a.scales ? a.scales[id] : 1.0f;
   const bool busy = p0 + 16 * wave < p1;
   // all of the wave's stores are made: they count among what a stage is waited for
@@ -676,7 +752,7 @@ __global__ __launch_bounds__(256) void k_lora_up_long(LoraLaunch a, int tiles, i
 
 template <int DT, int RS, bool ONE>
 __global__ __launch_bounds__(256) void k_lora_up(LoraLaunch a, int tiles, int slots, int n_per, int parts) {
-  __shared__ LoraT<DT, RS, ONE> shared[4][64];
+  __shared__ LoraUpLds<DT, RS, ONE> lds;
   LoraShare sh;
   if (!lora_share(tiles, parts, sh)) return;
   const LoraTile t = lora_tile(a, sh.tile);
@@ -688,11 +764,11 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraLaunch a, int tiles, int sl
     if (__builtin_amdgcn_readlane(t.id, p0) < 0)
       lora_copy(a, t, p0, p1, n0, n1);
     else if (p1 - p0 <= 16)
-      lora_up<DT, RS, ONE, 1>(a, t, sh.tile, p0, p1, n0, n1, shared);
+      lora_up<DT, RS, ONE, 1>(a, t, sh.tile, p0, p1, n0, n1, lds);
     else if (p1 - p0 <= 32)
-      lora_up<DT, RS, ONE, 2>(a, t, sh.tile, p0, p1, n0, n1, shared);
+      lora_up<DT, RS, ONE, 2>(a, t, sh.tile, p0, p1, n0, n1, lds);
     else
-      lora_up<DT, RS, ONE, 4>(a, t, sh.tile, p0, p1, n0, n1, shared);
+      lora_up<DT, RS, ONE, 4>(a, t, sh.tile, p0, p1, n0, n1, lds);
   }
 }
 
@@ -706,7 +782,7 @@ struct LoraPlan {
 // runs of K that the workspace has room for: none below 256 k
 static int lora_most_splits(int M, int K) {
   const int tiles = (M + LO_ROWS - 1) / LO_ROWS;
-  return std::max(1, std::min({K / 256, 512 / tiles, 16}));
+  return std::max(1, std::min({K / 256, 512 / tiles, kMostSplits}));
 }
 size_t lora_workspace(int M, int K, int rank) { return (size_t)lora_most_splits(M, K) * M * rank * sizeof(float); }
 
@@ -722,7 +798,12 @@ static LoraPlan lora_plan(const LoraLaunch& a) {
   int64_t down, up;  // parts wanted: one workgroup a CU beside the further slots, or two
   if (p.wide) {
     p.slots = (int)std::min<int64_t>(4, runs);
-    down = up = 256 / p.tiles;
+    up = 256 / p.tiles;
+    // the second kernel's waves sum all runs each, which costs more than shorter
+    // runs save (8 runs / 16, both kernels: 700 rows 1024 x 8192, rank 32, 16.2 / 23.4
+    // us; 1024 rows 8192 x 8192, rank 128, 36 / 42, rank 64 25.8 / 27.7); up to rank 16
+    // half the lanes take half of them (512 rows 18.1 / 16.4)
+    down = a.rank > 16 ? std::min<int64_t>(kLongSplits, up) : up;
   } else {
     p.slots = (int)std::min<int64_t>({32, a.M, LO_ROWS / p.tiles, runs});
     p.slots = std::max(p.slots, 1);
@@ -730,6 +811,7 @@ static LoraPlan lora_plan(const LoraLaunch& a) {
   }
   p.splits = std::max<int>(1, std::min<int64_t>(lora_most_splits(a.M, a.K), down));
   p.k_per = ((a.K + p.splits - 1) / p.splits + 63) / 64 * 64;
+  p.splits = (a.K + p.k_per - 1) / p.k_per;  // (the rounding may leave none for the last)
   const int64_t blocks = ((int64_t)a.N + 255) / 256, want = std::max<int64_t>(1, std::min(blocks, up));
   p.n_per = (blocks + want - 1) / want * 256;
   p.parts = (a.N + p.n_per - 1) / p.n_per;
