@@ -17,7 +17,7 @@
 //
 // Bound by memory and by what a launch takes to start (a first copy waits for
 // the row's place, then for its adapter's number): 4096 rows 22.9 + 37.4 us, the
-// second at 4.9 TB/s past the 7 us that it needs for any size; 16 rows of 16
+// second at 5.0 TB/s past the 7 us that it needs for any size; 16 rows of 16
 // adapters, rank 16, 4.3 + 5.4.
 #include <algorithm>
 

@@ -487,8 +487,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int w
 // group are a group of their own behind the others, whose counts go nowhere.
 // With one workgroup the places follow at once; otherwise the ranks wait in
 // `place` for k_group_place.
-// Latency bounds it: 64 rows 2.7 us (an empty launch 2.5), 131072 rows into 128
-// groups 3.8 and 6.7 in the second launch.
+// Latency bounds it: 64 rows 2.8 us (an empty launch 2.5), 131072 rows into 128
+// groups 4.0 and 6.6 in the second launch.
 __global__ __launch_bounds__(RT_THREADS) void k_group(GroupLaunch a) {
   __shared__ uint16_t hist[RT_THREADS / 64][kMaxGroups + 8];
   __shared__ int base[kMaxGroups + 8];
