@@ -49,7 +49,10 @@ def up(*tensors):
     (128, 520, 256, 72, 2, 64), (200, 136, 300 // 8 * 8, 128, 3, 20), (333, 2000, 2056, 40, 12, 7),
     (1000, 256, 768, 16, 300, 1), (700, 128, 4096, 48, 2, 350), (511, 264, 1032, 64, 6, 40),
     (512, 72, 40, 8, 3, 100), (513, 8, 8, 64, 5, 9), (900, 200, 2056, 72, 4, 130), (1500, 1032, 264, 128, 3, 200),
-    (640, 136, 1000, 32, 700, 1), (2048, 520, 4096, 24, 8, 300), (777, 328, 648, 96, 2, 64)])
+    (640, 136, 1000, 32, 700, 1), (2048, 520, 4096, 24, 8, 300), (777, 328, 648, 96, 2, 64),
+    # X A^T in more than eight runs of K: short runs of up to 16, 32 and 64 rows, long ones up to rank 16
+    (3, 200, 4104, 48, 2, 1), (9, 264, 8192, 16, 4, 1), (15, 72, 4352, 128, 1, 15), (30, 136, 4096, 24, 1, 30),
+    (50, 72, 4360, 128, 2, 25), (60, 200, 6000, 40, 1, 60), (64, 136, 4096, 16, 1, 64), (600, 72, 4608, 16, 3, 100)])
 def test_lora(gmi, dtype, M, N, K, rank, adapters, run):
     X, A, B, index, scales, base = case(M, N, K, rank, adapters, dtype, run=run)
     d = up(X, A, B, index, scales, base)
