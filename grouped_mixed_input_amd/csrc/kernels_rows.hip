@@ -16,7 +16,7 @@
 //
 // 16384 tokens, top 8, 4096 columns: permute (fp8) 106 to 111 us (5.6 to 5.9
 // TB/s), unpermute (bf16, with add) 242 (5.55), its gradient as codes 334 (5.3);
-// 131072 x 2 x 1024 bf16: gate 110 us (6.1 TB/s), its gradient 164 (6.4), where
+// 131072 x 2 x 1024 bf16: gate 111 us (6.1 TB/s), its gradient 168 (6.3), where
 // arithmetic takes as long as memory.  Rows of 4 KB far apart cost 15% over a
 // contiguous walk.  Few tokens: 3.6 us a launch, of which an empty one takes 2.5.
 #include "gmi_device.hpp"
@@ -262,14 +262,26 @@ __global__ __launch_bounds__(256) void k_unpermute_bwd(UnpermuteBwdLaunch a) {
 
 constexpr int kSwigluUnits = 2;
 
-// 1 / (1 + e^-g).  The rounding of g log2 e leaves |g| 2^-24 of e^-g, which
-// reaches the result where g is negative; all else is a few last bits.  Four
-// instructions, since arithmetic takes these kernels as long as memory: with
-// that rounding taken back (eight more) 120 us for 113 in the forward call of
-// 131072 x 2 x 1024, 186 for 168 in its gradient.  e^-g past the fp32 range
-// gives 0.
-__device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+// s = 1 / (1 + e^-g), and 1 - s as e^-g s, which cancels nothing.  e^-g as 2^t
+// with t = -g log2 e rounded, times e^r = 1 + r with r = -g - t ln 2: 2^t alone
+// would carry t's rounding, |g| 2^-24 of it.  What is left of that is |g| 2^-28,
+// ln 2 in fp32; exponential and reciprocal bring a last bit each.  From 88.5 on
+// e^-g would pass the fp32 range: the bound keeps it finite there, s is below
+// 2^-126, for which the reciprocal gives 0, and 1 - s comes out 0 with it, where
+// only its product with s is wanted; infinities would leave NaN in r.
+// (131072 x 2 x 1024, without r and with 1 - s as a difference: 110 us for 111 in
+// the forward call, 164 for 168 in its gradient.)
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+  constexpr float LOG2E = 1.44269504f, LN2 = 0.693147182f;
+  g = __builtin_amdgcn_fmed3f(g, -88.5f, 128.0f);
+  const float t = g * -LOG2E;
+  float e = __builtin_amdgcn_exp2f(t);
+  e = __builtin_fmaf(e, __builtin_fmaf(-LN2, t, -g), e);
+  const float s = __builtin_amdgcn_rcpf(1.0f + e);
+  return {s, e * s};
 }
 
 // unit / nb and the rest, by the multiplier that the launch brings
@@ -312,7 +324,7 @@ __global__ __launch_bounds__(256) void k_swiglu(SwigluLaunch a) {
     unpack8<DT>(uv[j], u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      g[e] = g[e] * sigmoid(g[e]) * u[e];
+      g[e] = g[e] * sigmoid(g[e]).s * u[e];
       amax = fmaxf(amax, fabsf(g[e]));
     }
     if (a.y && in[j]) store<NT>(a.y + row[j] * a.ldy + (int64_t)c[j] * 8, pack8<DT>(g));
@@ -349,9 +361,9 @@ __global__ __launch_bounds__(256) void k_swiglu_bwd(SwigluLaunch a) {
   float mg = 0.0f, mu = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float s = sigmoid(g[e]);
-    du[e] = d[e] * g[e] * s;
-    g[e] = d[e] * u[e] * s * __builtin_fmaf(g[e], 1.0f - s, 1.0f);
+    const Sigmoid sg = sigmoid(g[e]);
+    du[e] = d[e] * g[e] * sg.s;
+    g[e] = d[e] * u[e] * sg.s * __builtin_fmaf(g[e], sg.rest, 1.0f);
     if (up) g[e] = du[e];
     mg = fmaxf(mg, fabsf(g[e]));
     mu = fmaxf(mu, fabsf(du[e]));

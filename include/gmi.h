@@ -623,7 +623,8 @@ gmi_status gmi_moe_unpermute_bwd(int32_t tokens, int32_t k, int32_t K, gmi_dtype
                                  float* scales, int64_t lds, float* dweights, void* stream);
 
 /* Gated activation of the two halves of a row, for the next product:
- *   v = g / (1 + e^-g) * u,  g = a[r][0 .. N - 1], u = a[r][N .. 2 N - 1]   (fp32)
+ *   v = g / (1 + e^-g) * u,  g = a[r][0 .. N - 1], u = a[r][N .. 2 N - 1]   (fp32,
+ *   to its last bits; 1 / (1 + e^-g) below 2^-126, g < -87.3, counts as 0)
  *   y = RN(v); q = e4m3(v / s), s as for gmi_rmsnorm_quant.
  *   a      [rows][lda], lda >= 2 N, dtype GMI_F16 or GMI_BF16; N a multiple of
  *          8, at most 2^22.
