@@ -134,21 +134,15 @@ __global__ __launch_bounds__(256) void k_unpermute(UnpermuteLaunch a) {
   }
 }
 
-// sum + <a, b> over eight columns.  The bf16 product pair's instruction keeps
-// 2.2 fp32 roundings of its three terms' magnitudes (measured); fp16's drops
-// bits of subnormal operands and is not used.
+// sum + <a, b> over eight columns, each product of two 16-bit values added with
+// one fp32 rounding.  (The instructions for product pairs round otherwise: bf16's
+// is off by more where terms cancel, fp16's drops bits of subnormal operands.)
 template <int DT>
 __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float sum) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (DT == DT_BF16) {
-      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-      const uint32_t x = a[i], y = b[i];
-      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, x), __builtin_bit_cast(b2, y), sum, false);
-    } else {
-      sum = __builtin_fmaf(from_bits<DT>(a[i] & 0xffffu), from_bits<DT>(b[i] & 0xffffu), sum);
-      sum = __builtin_fmaf(from_bits<DT>(a[i] >> 16), from_bits<DT>(b[i] >> 16), sum);
-    }
+    sum = __builtin_fmaf(from_bits<DT>(a[i] & 0xffffu), from_bits<DT>(b[i] & 0xffffu), sum);
+    sum = __builtin_fmaf(from_bits<DT>(a[i] >> 16), from_bits<DT>(b[i] >> 16), sum);
   }
   return sum;
 }
