@@ -60,7 +60,12 @@ __device__ __forceinline__ int64_t part_at(const LoraLaunch& a, int64_t pos, int
   return LONG ? ((int64_t)(col >> 2) * a.M + pos) * 4 : pos * a.rank + col;
 }
 
-constexpr int kMostSplits = 16, kLongSplits = 8;  // runs of K; past rank 16 in the kernels for long runs
+// Runs of K at most; fewer past rank 16 in the kernels for long runs, where the
+// second kernel's waves sum all runs each, which costs more than shorter runs
+// save (8 runs / 16, both kernels: 700 rows 1024 x 8192, rank 32, 16.2 / 23.4 us;
+// 1024 rows 8192 x 8192, rank 128, 36 / 42, rank 64 25.8 / 27.7).  Up to rank 16
+// half the lanes take half of them (512 rows 18.1 / 16.4).
+constexpr int kMostSplits = 16, kLongSplits = 8;
 // 16 bytes, or zeros
 __device__ __forceinline__ u32x4 load_if(const uint16_t* p, bool in) { return in ? *(const u32x4*)p : u32x4{}; }
 
@@ -779,17 +784,20 @@ struct LoraPlan {
   int64_t parts, n_per;      // column blocks
   bool wide;                 // through LDS, for long runs
 };
-// runs of K that the workspace has room for: none below 256 k
-static int lora_most_splits(int M, int K) {
-  const int tiles = (M + LO_ROWS - 1) / LO_ROWS;
-  return std::max(1, std::min({K / 256, 512 / tiles, kMostSplits}));
+static bool lora_wide(int M) { return M >= 512; }
+// runs of K at most, which the workspace has room for: none below 256 k
+static int lora_most_splits(int M, int K, int rank) {
+  const int tiles = (M + LO_ROWS - 1) / LO_ROWS, most = lora_wide(M) && rank > 16 ? kLongSplits : kMostSplits;
+  return std::max(1, std::min({K / 256, (lora_wide(M) ? 256 : 512) / tiles, most}));
 }
-size_t lora_workspace(int M, int K, int rank) { return (size_t)lora_most_splits(M, K) * M * rank * sizeof(float); }
+size_t lora_workspace(int M, int K, int rank) {
+  return (size_t)lora_most_splits(M, K, rank) * M * rank * sizeof(float);
+}
 
 static LoraPlan lora_plan(const LoraLaunch& a) {
   LoraPlan p;
   p.tiles = (a.M + LO_ROWS - 1) / LO_ROWS;
-  p.wide = a.M >= 512;
+  p.wide = lora_wide(a.M);
   // twice the runs that sorted rows make of a tile on average, and one without an
   // adapter: a workgroup with two runs takes them one after the other (4096 rows
   // with tiles of two runs: 89 us for 60), one with none still has to find that
@@ -798,18 +806,13 @@ static LoraPlan lora_plan(const LoraLaunch& a) {
   int64_t down, up;  // parts wanted: one workgroup a CU beside the further slots, or two
   if (p.wide) {
     p.slots = (int)std::min<int64_t>(4, runs);
-    up = 256 / p.tiles;
-    // the second kernel's waves sum all runs each, which costs more than shorter
-    // runs save (8 runs / 16, both kernels: 700 rows 1024 x 8192, rank 32, 16.2 / 23.4
-    // us; 1024 rows 8192 x 8192, rank 128, 36 / 42, rank 64 25.8 / 27.7); up to rank 16
-    // half the lanes take half of them (512 rows 18.1 / 16.4)
-    down = a.rank > 16 ? std::min<int64_t>(kLongSplits, up) : up;
+    down = up = 256 / p.tiles;
   } else {
     p.slots = (int)std::min<int64_t>({32, a.M, LO_ROWS / p.tiles, runs});
     p.slots = std::max(p.slots, 1);
     down = up = 512 / (p.tiles * p.slots);
   }
-  p.splits = std::max<int>(1, std::min<int64_t>(lora_most_splits(a.M, a.K), down));
+  p.splits = std::max<int>(1, std::min<int64_t>(lora_most_splits(a.M, a.K, a.rank), down));
   p.k_per = ((a.K + p.splits - 1) / p.splits + 63) / 64 * 64;
   p.splits = (a.K + p.k_per - 1) / p.k_per;  // (the rounding may leave none for the last)
   const int64_t blocks = ((int64_t)a.N + 255) / 256, want = std::max<int64_t>(1, std::min(blocks, up));
