@@ -330,7 +330,9 @@ struct LoraLaunch {
   const int32_t *index, *order;  // order NULL: rows as they come
   uint16_t* Y;
   int64_t ldx, lda, a_stride, ldb, b_stride, ldbase, ldy;
-  float* part;  // [splits][rank / 4][M][4]: X A^T over runs of K, rows in the order of the call
+  // X A^T over runs of K, rows in the order of the call: [splits][M][rank], or
+  // [splits][rank / 4][M][4] in the kernels for long runs (M >= 512)
+  float* part;
   int splits;
 };
 constexpr int kMaxLoraRank = 128;
