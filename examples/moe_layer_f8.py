@@ -21,15 +21,6 @@ import grouped_mixed_input_amd as gmi  # noqa: E402
 F8 = torch.float8_e4m3fn
 
 
-def quantize(v):
-    """fp8 codes and scales of a [rows][K] matrix, per row and 128 columns (plain torch: weights, once)."""
-    rows, K = v.shape
-    nb = -(-K // gmi.BLOCK)
-    b = torch.nn.functional.pad(v.float(), (0, nb * gmi.BLOCK - K)).view(rows, nb, gmi.BLOCK)
-    s = b.abs().amax(2).clamp_min(1e-30) / 448.0
-    return (b / s[:, :, None]).view(rows, -1)[:, :K].to(F8), s
-
-
 def quantize_weight(w):
     """fp8 codes and scales of [experts][N][K] weights, per 128 x 128 block."""
     E, N, K = w.shape
