@@ -1087,6 +1087,13 @@ static gmi_status row_operand(const char* who, const char* name, const void* p, 
                 unit);
   return GMI_OK;
 }
+// an output that may be an input exactly: rows apart otherwise would be written over rows still to be read
+static gmi_status in_place(const char* who, const char* names, const void* out, int64_t ldout, const void* p, int64_t ld,
+                           int64_t rows) {
+  if (out && out == p && ldout != ld && rows > 1)
+    return fail(GMI_ERR_INVALID_ARG, "%s: %s only with its leading dimension", who, names);
+  return GMI_OK;
+}
 // codes [rows][ldq] of `cols` columns with their scales [rows][lds]
 static gmi_status code_operand(const char* who, const void* q, int64_t ldq, const float* scales, int64_t lds,
                                int64_t cols) {
@@ -1193,7 +1200,8 @@ gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dty
   if (st != GMI_OK || tokens == 0) return st;
   if ((rows > 0 && (st = row_operand(who, "y", y, ldy, K)) != GMI_OK) ||
       (st = slot_rows(who, slot_row)) != GMI_OK || (add && (st = row_operand(who, "add", add, ldadd, K)) != GMI_OK) ||
-      (st = row_operand(who, "out", out, ldo, K)) != GMI_OK)
+      (st = row_operand(who, "out", out, ldo, K)) != GMI_OK ||
+      (st = in_place(who, "out may be add", out, ldo, add, ldadd, tokens)) != GMI_OK)
     return st;
   if (!aligned(weights, 4)) return fail(GMI_ERR_MISALIGNED, "%s: weights must be 4-byte aligned", who);
   UnpermuteLaunch a{};
@@ -1227,7 +1235,10 @@ gmi_status gmi_moe_unpermute_bwd(int32_t tokens, int32_t k, int32_t K, gmi_dtype
     return fail(GMI_ERR_INVALID_ARG, "%s: drows, or q with scales, or dweights alone", who);
   if (rows > 0 && drows && (st = row_operand(who, "drows", drows, lddrows, K)) != GMI_OK) return st;
   if (rows > 0 && coded && (st = code_operand(who, q, ldq, scales, lds, K)) != GMI_OK) return st;
-  if (dweights && rows > 0 && (st = row_operand(who, "y", y, ldy, K)) != GMI_OK) return st;
+  if (dweights && rows > 0 &&
+      ((st = row_operand(who, "y", y, ldy, K)) != GMI_OK ||
+       (st = in_place(who, "drows may be y", drows, lddrows, y, ldy, rows)) != GMI_OK))
+    return st;
   if (!aligned(weights, 4) || !aligned(dweights, 4))
     return fail(GMI_ERR_MISALIGNED, "%s: weights and dweights must be 4-byte aligned", who);
   if (rows == 0 && !dweights) return GMI_OK;
@@ -1299,7 +1310,8 @@ gmi_status gmi_swiglu_bwd(int32_t rows, int32_t N, gmi_dtype dtype, const void* 
   if ((st = row_operand(who, "dact", dact, lddact, N)) != GMI_OK ||
       (st = row_operand(who, "a", a_, lda, 2 * (int64_t)N)) != GMI_OK ||
       (st = da ? row_operand(who, "da", da, ldda, 2 * (int64_t)N)
-               : code_operand(who, q, ldq, scales, lds, 2 * (int64_t)N)) != GMI_OK)
+               : code_operand(who, q, ldq, scales, lds, 2 * (int64_t)N)) != GMI_OK ||
+      (st = in_place(who, "da may be a", da, ldda, a_, lda, rows)) != GMI_OK)
     return st;
   SwigluLaunch a{};
   a.rows = rows;
@@ -1352,8 +1364,7 @@ gmi_status gmi_gemm_lora(int32_t M, int32_t N, int32_t K, int32_t rank, int32_t 
       (base && (st = row_operand(who, "base", base, ldbase, N)) != GMI_OK) ||
       (st = row_operand(who, "Y", Y, ldy, N)) != GMI_OK)
     return st;
-  if (base == Y && ldbase != ldy)
-    return fail(GMI_ERR_INVALID_ARG, "%s: Y may be base only with its leading dimension", who);
+  if ((st = in_place(who, "Y may be base", Y, ldy, base, ldbase, M)) != GMI_OK) return st;
   if (adapters > 0) {
     if ((st = row_operand(who, "A", A, lda, K)) != GMI_OK || (st = row_operand(who, "B", B, ldb, rank)) != GMI_OK)
       return st;

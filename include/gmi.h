@@ -596,7 +596,7 @@ gmi_status gmi_moe_permute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype
  *   y        [rows][ldy]; out [tokens][ldo]; `dtype` (GMI_F16 or GMI_BF16).
  *   weights  fp32 [tokens][k], or NULL for 1.
  *   add      [tokens][ldadd] (a shared expert, the residual stream) or NULL;
- *            out may be add exactly.
+ *            out may be add exactly (same pointer and leading dimension).
  * K a multiple of 8; other sizes as for gmi_moe_permute. */
 gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dtype, const void* y, int64_t ldy,
                              int32_t rows, const int32_t* slot_row, const float* weights, const void* add,
@@ -613,7 +613,7 @@ gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dty
  *   drows      [rows][lddrows], `dtype`; or NULL, and q fp8 [rows][ldq] (8-byte
  *              aligned, ldq a multiple of 8, of 16 where a GEMM call reads it)
  *              with scales fp32 [rows][lds]; or none of them (dweights alone).
- *              drows may be y exactly.
+ *              drows may be y exactly (same pointer and leading dimension).
  *   dweights   fp32 [tokens][k] or NULL (a frozen router).
  * A NaN among g stands in q and does not enter the block's maximum.  Rows that
  * no slot has are not written.  Sizes as for gmi_moe_unpermute. */
@@ -642,7 +642,8 @@ gmi_status gmi_swiglu_quant(int32_t rows, int32_t N, gmi_dtype dtype, const void
  *        (a block of 128 may hold the end of dg and the start of du).
  *   dact   [rows][lddact], `dtype`.
  *   da     [rows][ldda], `dtype`; or NULL, and q fp8 [rows][ldq] with scales
- *          fp32 [rows][lds], lds >= ceil(2 N / 128).  da may be a exactly.
+ *          fp32 [rows][lds], lds >= ceil(2 N / 128).  da may be a exactly (same
+ *          pointer and leading dimension).
  * Other arguments as for gmi_swiglu_quant. */
 gmi_status gmi_swiglu_bwd(int32_t rows, int32_t N, gmi_dtype dtype, const void* dact, int64_t lddact, const void* a,
                           int64_t lda, const int32_t* live, void* da, int64_t ldda, void* q, int64_t ldq, float* scales,
