@@ -411,7 +411,10 @@ __device__ __forceinline__ void sum_counts(const uint16_t* counts, int ld, int E
 // Latency is what it costs, so the slots are fetched before the matrix, the
 // matrix is 16 bits wide and read eight experts a load: with 256 workgroups and
 // 128 experts four loads a thread (32-bit, one expert a load: 15.9 us).
-__global__ __launch_bounds__(RT_THREADS) void k_route_place(RouteLaunch a, int wgs) {
+// Eight waves a SIMD: the further workgroup has to find room beside another one
+// on a device that the rest fill (with 79 registers and so one workgroup a CU
+// the call of 16384 tokens x 128 took 18.8 us for 17.0).
+__global__ __launch_bounds__(RT_THREADS, 8) void k_route_place(RouteLaunch a, int wgs) {
   __shared__ int32_t part[2][8 * RT_THREADS];  // partial totals and prefixes, then floats of the sums of p
   __shared__ int row0[RT_THREADS];
   __shared__ int wave_i[RT_THREADS / 64];
