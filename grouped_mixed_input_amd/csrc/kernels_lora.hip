@@ -784,6 +784,8 @@ struct LoraPlan {
   int64_t parts, n_per;      // column blocks
   bool wide;                 // through LDS, for long runs
 };
+// The border is that of 8 adapters (the figures at the head): with hundreds of
+// them runs stay short from 512 rows on too, which was not timed.
 static bool lora_wide(int M) { return M >= 512; }
 // runs of K at most, which the workspace has room for: none below 256 k
 static int lora_most_splits(int M, int K, int rank) {

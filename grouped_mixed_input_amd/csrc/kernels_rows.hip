@@ -399,8 +399,11 @@ static unsigned wave_grid(int64_t waves) {
 }
 
 // Accesses past the caches (loads of what is read once, stores), by the bytes
-// of the largest tensor.  4096 columns, top 8, inner 1024, us alone and with the
-// grouped product that writes the input or reads the result (through / past):
+// of the largest tensor.  One border for all: the gate and its gradient would gain
+// half a microsecond at 4 MB, alone, and nothing with the product beside them.
+// 4096 columns, top 8, inner 1024, us alone and with the grouped product that
+// writes the input or reads the result (through / past; the gates' with a sigmoid
+// that was three instructions shorter):
 //                 64 tokens (4 MB)         256 (17 MB)             4096 (268 MB)         16384
 //   permute       5.2, 171 / 5.7, 169      5.8, 186 / 5.9, 182     32.7, 478 / 28.7, 450  124 / 107
 //   unpermute     5.3, 99 / 5.5, 99        6.9, 112 / 6.0, 112     61, 335 / 53.5, 322    239 / 211

@@ -606,6 +606,8 @@ gmi_status gmi_moe_unpermute(int32_t tokens, int32_t k, int32_t K, gmi_dtype dty
  *   g = weights[t][i] * dout[t]          (fp32) for row slot_row[t][i]
  *   drows = RN(g), or q = e4m3(g / s) with s = max(max |g| over the 128-column
  *   block, 448 * 2^-126) / 448, the fp8 operand of the data gradient's product
+ *   (a weight whose products leave no range cancels in g / s: its codes are those
+ *   of 448 dout / max |dout|, with its sign, free of the roundings of g and s)
  *   dweights[t][i] = sum over columns of dout[t] * y[slot_row[t][i]]   (fp32; 0
  *   for a slot without a row)
  *   dout       [tokens][lddout], `dtype`.
